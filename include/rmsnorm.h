@@ -298,6 +298,204 @@ rmsnorm_status_t rmsnorm_bwd_noalloc(const void* dy, const void* x, const float*
 rmsnorm_status_t rmsnorm_check_device(cudaStream_t stream);
 
 /*
+ * Rotary positions with several axes (time, height, width, ...) over the heads
+ * of q and k, alone or behind the per-head RMSNorm of rmsnorm_fwd_strided.
+ *
+ * A [T, H, D] view: element (t, h, d) at data[t * stride_token + h *
+ * stride_head + d].  Strides are in elements, non-negative, and the rows of a
+ * view must not overlap (as in rmsnorm_fwd_strided).
+ */
+typedef struct rmsnorm_heads {
+  void* data;            /* device pointer */
+  int64_t stride_token;
+  int64_t stride_head;
+  int64_t heads;         /* H */
+} rmsnorm_heads_t;
+
+#define RMSNORM_ROPE_MAX_AXES 4
+#define RMSNORM_ROPE_MAX_D 8192
+
+typedef enum rmsnorm_rope_pairs {
+  RMSNORM_ROPE_HALVES = 0,   /* column i turns with column i + R / 2 */
+  RMSNORM_ROPE_ADJACENT = 1  /* column 2i turns with column 2i + 1 */
+} rmsnorm_rope_pairs_t;
+
+typedef enum rmsnorm_rope_order {
+  RMSNORM_ROPE_BLOCKS = 0,     /* the first sections[0] frequencies turn by axis 0, the next
+                                  sections[1] by axis 1, ... */
+  RMSNORM_ROPE_INTERLEAVED = 1 /* frequency i turns by axis a = i % axes while
+                                  i < sections[a] * axes, else by axis 0 */
+} rmsnorm_rope_order_t;
+
+/*
+ * The rotation: the first R = rotary_dim columns of every row turn, the others
+ * pass unchanged.  Frequency i < R / 2 turns its pair (u, v) at token t by
+ *     theta = positions[axis(i) * positions_stride + t] * inv_freq[i]
+ * to (u cos theta - v sin theta, u sin theta + v cos theta).  The product is
+ * taken as 64-bit fixed point modulo one turn, so angles keep their 32-bit
+ * accuracy at any position of magnitude below 2^31 (negative ones too).
+ * inv_freq must be finite.  `sections` and the other fields are read by the
+ * call (host); `positions` and `inv_freq` are device pointers.
+ */
+typedef struct rmsnorm_rope {
+  const int64_t* positions;  /* [axes, T] */
+  int64_t positions_stride;  /* elements from one axis to the next, >= T when axes > 1 */
+  const float* inv_freq;     /* [R / 2] */
+  int64_t rotary_dim;        /* R: even, 2 <= R <= D */
+  int32_t axes;              /* 1 .. RMSNORM_ROPE_MAX_AXES */
+  int32_t sections[RMSNORM_ROPE_MAX_AXES]; /* frequencies per axis, >= 0; the first `axes`
+                                              of them add up to R / 2 (and each axis' interleaved
+                                              frequencies must exist) */
+  int32_t pairs;             /* rmsnorm_rope_pairs_t */
+  int32_t order;             /* rmsnorm_rope_order_t */
+} rmsnorm_rope_t;
+
+/*
+ * q_out = rope(norm(q)), k_out = rope(norm(k)) in one launch, for q [T, Hq, D]
+ * and k [T, Hk, D]; k may be NULL (then k_gamma and k_out too).  norm is
+ * x / sqrt(mean(x^2) + eps) * gamma over each row's D elements with q_gamma and
+ * k_gamma (D values, w_dtype); with both NULL it is left out and eps and
+ * w_dtype are not used.  Everything between reading x and rounding the result
+ * is fp32.  An output may be its input with the same strides (in place);
+ * otherwise no output shares memory with another operand.  Views cut side by
+ * side out of one buffer are apart: q and k of a fused projection's rows (equal
+ * token strides), or heads in turn (equal head strides that divide the token
+ * strides).  D <= RMSNORM_ROPE_MAX_D,
+ * T < 2^30, Hq + Hk <= 2^16.  Rows whose starts, strides and halves fall on
+ * 16-byte vectors (D and R multiples of two vectors, 32 bytes), of at most
+ * 64 vectors, take the vectorised kernels; any other layout a scalar one.
+ */
+rmsnorm_status_t rmsnorm_rope_fwd(const rmsnorm_heads_t* q, const rmsnorm_heads_t* k,
+                                  const void* q_gamma, const void* k_gamma,
+                                  const rmsnorm_heads_t* q_out, const rmsnorm_heads_t* k_out,
+                                  const rmsnorm_rope_t* rope, int64_t T, int64_t D, float eps,
+                                  rmsnorm_dtype_t x_dtype, rmsnorm_dtype_t w_dtype,
+                                  cudaStream_t stream);
+
+/* Bytes of device workspace rmsnorm_rope_bwd needs for the weight gradients at
+ * these sizes on `device` (-1: the current device), written to *bytes.  k_heads
+ * is 0 without k. */
+rmsnorm_status_t rmsnorm_rope_bwd_workspace_size(int64_t T, int64_t q_heads, int64_t k_heads,
+                                                 int64_t D, rmsnorm_dtype_t x_dtype,
+                                                 rmsnorm_dtype_t w_dtype, int device,
+                                                 size_t* bytes);
+
+/*
+ * Backward of rmsnorm_rope_fwd.  With g = dq_out turned back by -theta (the
+ * unrotated columns as they are):
+ *     without the norm  dq = g
+ *     with it           c = rstd^2 / D sum_j gamma_j g_j q_j
+ *                       dq = rstd (gamma g - q c),  dq_gamma = sum over rows of g q rstd
+ * and the same for k.  q, k: the forward's inputs (NULL without the norm, which
+ * does not need them); rstd is recomputed from them with the forward's eps.
+ * dq may be dq_out with the same strides (in place).  dq_gamma, dk_gamma: D
+ * fp32 each, either may be NULL to skip it; summed in a fixed order through
+ * `workspace` (at least rmsnorm_rope_bwd_workspace_size bytes, 16-byte
+ * aligned; unused when both are NULL).  dk_out, k, dk, k_gamma and dk_gamma are
+ * NULL without k.  With no rows the wanted weight gradients are set to zero.
+ */
+rmsnorm_status_t rmsnorm_rope_bwd(const rmsnorm_heads_t* dq_out, const rmsnorm_heads_t* dk_out,
+                                  const rmsnorm_heads_t* q, const rmsnorm_heads_t* k,
+                                  const void* q_gamma, const void* k_gamma,
+                                  const rmsnorm_heads_t* dq, const rmsnorm_heads_t* dk,
+                                  float* dq_gamma, float* dk_gamma, void* workspace,
+                                  size_t workspace_bytes, const rmsnorm_rope_t* rope, int64_t T,
+                                  int64_t D, float eps, rmsnorm_dtype_t x_dtype,
+                                  rmsnorm_dtype_t w_dtype, cudaStream_t stream);
+
+/*
+ * Log-probability of each row's target token, the step from a model's logits
+ * to the losses below.  With z = logits * inv_temperature (inv_temperature
+ * finite and > 0):
+ *     lse_i = log sum_j exp(z_ij),     logp_i = z_i,target(i) - lse_i
+ * logits: M rows of V elements (x_dtype), row i at logits + i * ld (ld >= V
+ * when M > 1; rows need not start on 16 bytes); targets: M int64; logp, lse: M
+ * fp32 each.  A negative target leaves its row out: it is not read, logp and
+ * lse are 0, and its gradient is zero.  A target >= V gives NaN (in logp, in
+ * the losses and in the row's gradient).  Sums are fp32 over values scaled by
+ * the row's maximum; lse and logp are put together in 64 bits and rounded once.
+ * Logits of -inf have probability 0; a row of nothing else, or with a NaN or
+ * +inf, gives NaN.  M < 2^28.  No workspace.
+ */
+rmsnorm_status_t rmsnorm_token_logprob_fwd(const void* logits, int64_t ld,
+                                           const int64_t* targets, double inv_temperature,
+                                           float* logp, float* lse, int64_t M, int64_t V,
+                                           rmsnorm_dtype_t x_dtype, cudaStream_t stream);
+
+/*
+ * Gradient of the logits from the gradient of logp -- the backward of
+ * rmsnorm_token_logprob_fwd, rmsnorm_policy_loss_fwd and
+ * rmsnorm_preference_loss_fwd:
+ *     dlogits_ij = scale * dlogp_i * inv_temperature * ([j = target(i)] - exp(z_ij - lse_i))
+ * lse: the forward's; dlogp: M fp32 (the losses' forwards write it); scale: one
+ * fp32 on the device (the loss's own upstream gradient), or NULL for 1.
+ * dlogits: M rows of V (x_dtype), row stride ld_out; it may be logits itself
+ * with ld_out = ld (in place).  Rows that are left out, and rows whose dlogp or
+ * scale is 0, are set to zero without being read.  A row whose start differs
+ * from its logits' modulo 16 bytes takes a scalar path.
+ */
+rmsnorm_status_t rmsnorm_token_logprob_bwd(const void* logits, int64_t ld,
+                                           const int64_t* targets, double inv_temperature,
+                                           const float* lse, const float* dlogp,
+                                           const float* scale, void* dlogits, int64_t ld_out,
+                                           int64_t M, int64_t V, rmsnorm_dtype_t x_dtype,
+                                           cudaStream_t stream);
+
+/*
+ * Clipped policy loss with an optional KL term, over the rows whose target is
+ * not negative:
+ *     r_i    = exp(logp_i - old_logp_i),   A_i = advantages_i,   w_i = weights_i
+ *     s_i    = A_i min(r_i, 1 + clip_high)   for A_i >= 0,
+ *              A_i max(r_i, 1 - clip_low)    for A_i < 0
+ *     kl_i   = exp(ref_logp_i - logp_i) - (ref_logp_i - logp_i) - 1
+ *     token_loss_i = w_i (kl_coef kl_i - s_i),      loss = sum_i token_loss_i
+ *     dlogp_i = w_i (-A_i r_i [r_i not clipped] - kl_coef (exp(ref_logp_i - logp_i) - 1))
+ * old_logp, advantages: M fp32; weights: M fp32 or NULL for 1 (a mean over the
+ * live tokens is weights of 1 / their number; a row of weight 0 is worth 0 even
+ * where its other values are not finite); ref_logp: M fp32, or NULL for no KL term (kl_coef is
+ * then not used).  clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, all finite.
+ * loss: one fp32; token_loss, logp, lse, dlogp: M fp32 each.  dlogits: M rows
+ * of V (x_dtype, row stride ld_out; logits itself with ld_out = ld for in
+ * place) for the gradient of loss in the same pass -- each row of logits is
+ * read from memory once and written once -- or NULL; the gradient for another
+ * upstream factor comes from rmsnorm_token_logprob_bwd.  Sums are taken in a
+ * fixed order: the same inputs give the same bits.  With M = 0 loss is 0.
+ */
+rmsnorm_status_t rmsnorm_policy_loss_fwd(const void* logits, int64_t ld, const int64_t* targets,
+                                         double inv_temperature, const float* old_logp,
+                                         const float* ref_logp, const float* advantages,
+                                         const float* weights, float clip_low, float clip_high,
+                                         float kl_coef, float* loss, float* token_loss,
+                                         float* logp, float* lse, float* dlogp, void* dlogits,
+                                         int64_t ld_out, int64_t M, int64_t V,
+                                         rmsnorm_dtype_t x_dtype, cudaStream_t stream);
+
+/*
+ * Preference loss of paired log ratios.  The rows hold 2 * pairs sequences
+ * end to end, sequence s in rows [cu_seqlens[s], cu_seqlens[s + 1]): the chosen
+ * answers s = 0 .. pairs - 1, then the rejected ones in the same order; rows
+ * before the first and behind the last offset belong to none.  With
+ *     S_s = sum over the sequence's rows with a target of (logp_i - ref_logp_i)
+ *     margin_b = beta (S_b - S_{pairs + b})
+ *     loss = 1 / pairs sum_b ( (1 - label_smoothing) log(1 + exp(-margin_b))
+ *                              + label_smoothing log(1 + exp(margin_b)) )
+ * and dlogp_i the derivative of loss by logp_i (0 in rows of no sequence).
+ * ref_logp: M fp32 per token, or NULL for 0.  cu_seqlens: 2 * pairs + 1 int64
+ * on the device, not decreasing, within [0, M] (offsets outside are cut to the
+ * batch); an empty sequence has S = 0.  S and the margins are summed in 64 bits.
+ * 1 <= pairs < 2^24, beta finite, 0 <= label_smoothing <= 1.  loss: one fp32;
+ * margins: `pairs` fp32; logp, lse, dlogp: M fp32 each.  The gradient of the
+ * logits comes from rmsnorm_token_logprob_bwd.
+ */
+rmsnorm_status_t rmsnorm_preference_loss_fwd(const void* logits, int64_t ld,
+                                             const int64_t* targets, double inv_temperature,
+                                             const float* ref_logp, const int64_t* cu_seqlens,
+                                             int64_t pairs, float beta, float label_smoothing,
+                                             float* loss, float* margins, float* logp, float* lse,
+                                             float* dlogp, int64_t M, int64_t V,
+                                             rmsnorm_dtype_t x_dtype, cudaStream_t stream);
+
+/*
  * Text naming the CUDA call that failed and its error, for the last
  * RMSNORM_ERR_CUDA returned to the calling thread ("" if none).  The string
  * belongs to the library and stays valid until that thread's next call.

@@ -23,7 +23,10 @@ __all__ = ["F32", "BF16", "OP_FWD", "OP_FUSED_ADD", "OP_BWD", "OP_FUSED_ADD_BWD"
            "load_library", "rmsnorm_fwd", "rmsnorm_fused_add_fwd", "rmsnorm_bwd",
            "rmsnorm_bwd_workspace_size", "rmsnorm_status_string", "rmsnorm_describe_plan",
            "rmsnorm_bwd_noalloc", "NOALLOC_SCRATCH_BYTES", "rmsnorm_check_device",
-           "rmsnorm_last_error", "rmsnorm_reload_debug_env", "EXPORTED_SYMBOLS"]
+           "rmsnorm_last_error", "rmsnorm_reload_debug_env", "EXPORTED_SYMBOLS", "Heads", "Rope",
+           "rmsnorm_rope_fwd", "rmsnorm_rope_bwd_workspace_size", "rmsnorm_rope_bwd",
+           "rmsnorm_token_logprob_fwd", "rmsnorm_token_logprob_bwd", "rmsnorm_policy_loss_fwd",
+           "rmsnorm_preference_loss_fwd"]
 
 F32 = 0
 BF16 = 1
@@ -37,7 +40,10 @@ EXPORTED_SYMBOLS = ("rmsnorm_fwd", "rmsnorm_fused_add_fwd", "rmsnorm_bwd_workspa
                     "rmsnorm_bwd_noalloc", "rmsnorm_check_device", "rmsnorm_last_error",
                     "rmsnorm_fused_add_bwd", "rmsnorm_fwd_strided", "rmsnorm_fwd_fp8",
                     "rmsnorm_fwd_nvfp4", "layernorm_fwd", "layernorm_bwd_workspace_size",
-                    "layernorm_bwd", "rmsnorm_reload_debug_env")
+                    "layernorm_bwd", "rmsnorm_reload_debug_env", "rmsnorm_rope_fwd",
+                    "rmsnorm_rope_bwd_workspace_size", "rmsnorm_rope_bwd",
+                    "rmsnorm_token_logprob_fwd", "rmsnorm_token_logprob_bwd",
+                    "rmsnorm_policy_loss_fwd", "rmsnorm_preference_loss_fwd")
 
 # Size of the library-owned scratch of rmsnorm_bwd_noalloc (16 MiB).
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -101,6 +107,26 @@ def load_library():
             lib.rmsnorm_fwd_fp8.restype = I
             lib.rmsnorm_fwd_nvfp4.argtypes = [P, P, P, F, P, P, P, I64, I64, F, I, I, P]
             lib.rmsnorm_fwd_nvfp4.restype = I
+            lib.rmsnorm_rope_fwd.argtypes = [P, P, P, P, P, P, P, I64, I64, F, I, I, P]
+            lib.rmsnorm_rope_fwd.restype = I
+            lib.rmsnorm_rope_bwd_workspace_size.argtypes = [I64, I64, I64, I64, I, I, I,
+                                                            ctypes.POINTER(SZ)]
+            lib.rmsnorm_rope_bwd_workspace_size.restype = I
+            lib.rmsnorm_rope_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, SZ, P, I64, I64, F,
+                                             I, I, P]
+            lib.rmsnorm_rope_bwd.restype = I
+            DBL = ctypes.c_double
+            lib.rmsnorm_token_logprob_fwd.argtypes = [P, I64, P, DBL, P, P, I64, I64, I, P]
+            lib.rmsnorm_token_logprob_fwd.restype = I
+            lib.rmsnorm_token_logprob_bwd.argtypes = [P, I64, P, DBL, P, P, P, P, I64, I64, I64, I,
+                                                      P]
+            lib.rmsnorm_token_logprob_bwd.restype = I
+            lib.rmsnorm_policy_loss_fwd.argtypes = [P, I64, P, DBL, P, P, P, P, F, F, F, P, P, P, P,
+                                                    P, P, I64, I64, I64, I, P]
+            lib.rmsnorm_policy_loss_fwd.restype = I
+            lib.rmsnorm_preference_loss_fwd.argtypes = [P, I64, P, DBL, P, P, I64, F, F, P, P, P, P,
+                                                        P, I64, I64, I, P]
+            lib.rmsnorm_preference_loss_fwd.restype = I
             lib.rmsnorm_last_error.argtypes = []
             lib.rmsnorm_last_error.restype = ctypes.c_char_p
             lib.rmsnorm_reload_debug_env.argtypes = []
@@ -115,6 +141,66 @@ def _ptr(a):
     if isinstance(a, int):
         return a
     return int(a.data_ptr())
+
+
+class Heads(ctypes.Structure):
+    """A [T, H, D] view of q or k (rmsnorm_heads_t): the device address of its first
+    element, the element strides of tokens and heads, and H.  `Heads.of(t)` takes
+    them from a torch tensor of that shape whose last dimension is contiguous."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("heads", ctypes.c_int64)]
+
+    def __init__(self, data, stride_token, stride_head, heads):
+        super().__init__(_ptr(data), stride_token, stride_head, heads)
+        self._keep = data
+
+    @classmethod
+    def of(cls, t):
+        if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+            raise ValueError("a [T, H, D] tensor with a contiguous last dimension is wanted")
+        return cls(t, t.stride(0), t.stride(1), t.shape[1])
+
+
+class Rope(ctypes.Structure):
+    """Rotary positions (rmsnorm_rope_t).  positions: int64 [axes, T] (or [T] for one
+    axis); inv_freq: float32 [rotary_dim / 2]; sections: frequencies per axis; pairs:
+    "halves" or "adjacent"; order: "blocks" or "interleaved".  Device tensors (kept
+    alive by this object), or raw addresses with positions_stride given."""
+    _fields_ = [("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_int64),
+                ("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int64),
+                ("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("pairs", ctypes.c_int32), ("order", ctypes.c_int32)]
+    _PAIRS = {"halves": 0, "adjacent": 1}
+    _ORDERS = {"blocks": 0, "interleaved": 1}
+
+    def __init__(self, positions, inv_freq, sections, rotary_dim, pairs="halves",
+                 order="blocks", positions_stride=None):
+        sections = tuple(sections)
+        if not 1 <= len(sections) <= 4:
+            raise ValueError("one to four axes are supported")
+        if positions_stride is None:
+            if positions.dim() == 2 and positions.shape[0] != len(sections):
+                raise ValueError(f"positions must have a row for each of the {len(sections)} axes")
+            if positions.dim() not in (1, 2) or (positions.dim() == 1 and len(sections) > 1):
+                raise ValueError("positions must be [axes, T], or [T] for one axis")
+            if positions.stride(-1) != 1 and positions.shape[-1] > 1:
+                raise ValueError("positions must be contiguous along the tokens")
+            positions_stride = positions.stride(0) if positions.dim() == 2 else 0
+        if hasattr(positions, "dtype") and str(positions.dtype) != "torch.int64":
+            raise TypeError(f"positions must be int64, got {positions.dtype}")
+        if hasattr(inv_freq, "dtype"):
+            if str(inv_freq.dtype) != "torch.float32" or not inv_freq.is_contiguous():
+                raise TypeError("inv_freq must be a contiguous float32 tensor")
+            if 2 * inv_freq.numel() < rotary_dim:
+                raise ValueError(f"inv_freq must hold {rotary_dim // 2} frequencies")
+        super().__init__(_ptr(positions), positions_stride, _ptr(inv_freq), rotary_dim,
+                         len(sections), (ctypes.c_int32 * 4)(*sections), self._PAIRS[pairs],
+                         self._ORDERS[order])
+        self._keep = (positions, inv_freq)
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
 
 
 def _stream(s):
@@ -233,6 +319,75 @@ def rmsnorm_bwd_noalloc(dy, x, rstd, gamma, dx, dgamma, M, N, eps, x_dtype, w_dt
                                               _ptr(dx), _ptr(dgamma), M, N, eps, _dt(x_dtype),
                                               _dt(w_dtype), _stream(stream)),
            "rmsnorm_bwd_noalloc")
+
+
+def rmsnorm_rope_fwd(q, k, q_gamma, k_gamma, q_out, k_out, rope, T, D, eps, x_dtype, w_dtype,
+                     stream=None):
+    """Rotary positions over q and k ([T, H, D] views as Heads; k may be None),
+    behind the per-head RMSNorm unless both gammas are None."""
+    _check(load_library().rmsnorm_rope_fwd(_ref(q), _ref(k), _ptr(q_gamma), _ptr(k_gamma),
+                                           _ref(q_out), _ref(k_out), _ref(rope), T, D, eps,
+                                           _dt(x_dtype), _dt(w_dtype), _stream(stream)),
+           "rmsnorm_rope_fwd")
+
+
+def rmsnorm_rope_bwd_workspace_size(T, q_heads, k_heads, D, x_dtype, w_dtype, device=-1) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().rmsnorm_rope_bwd_workspace_size(T, q_heads, k_heads, D, _dt(x_dtype),
+                                                          _dt(w_dtype), device,
+                                                          ctypes.byref(out)),
+           "rmsnorm_rope_bwd_workspace_size")
+    return int(out.value)
+
+
+def rmsnorm_rope_bwd(dq_out, dk_out, q, k, q_gamma, k_gamma, dq, dk, dq_gamma, dk_gamma,
+                     workspace, workspace_bytes, rope, T, D, eps, x_dtype, w_dtype, stream=None):
+    _check(load_library().rmsnorm_rope_bwd(_ref(dq_out), _ref(dk_out), _ref(q), _ref(k),
+                                           _ptr(q_gamma), _ptr(k_gamma), _ref(dq), _ref(dk),
+                                           _ptr(dq_gamma), _ptr(dk_gamma), _ptr(workspace),
+                                           workspace_bytes, _ref(rope), T, D, eps, _dt(x_dtype),
+                                           _dt(w_dtype), _stream(stream)),
+           "rmsnorm_rope_bwd")
+
+
+def rmsnorm_token_logprob_fwd(logits, ld, targets, inv_temperature, logp, lse, M, V, x_dtype,
+                              stream=None):
+    """logp and lse of each row's target token (rows of V logits, row stride ld)."""
+    _check(load_library().rmsnorm_token_logprob_fwd(_ptr(logits), ld, _ptr(targets),
+                                                    inv_temperature, _ptr(logp), _ptr(lse), M, V,
+                                                    _dt(x_dtype), _stream(stream)),
+           "rmsnorm_token_logprob_fwd")
+
+
+def rmsnorm_token_logprob_bwd(logits, ld, targets, inv_temperature, lse, dlogp, scale, dlogits,
+                              ld_out, M, V, x_dtype, stream=None):
+    """The logits' gradient from dlogp (times the device scalar `scale`, None for 1)."""
+    _check(load_library().rmsnorm_token_logprob_bwd(_ptr(logits), ld, _ptr(targets),
+                                                    inv_temperature, _ptr(lse), _ptr(dlogp),
+                                                    _ptr(scale), _ptr(dlogits), ld_out, M, V,
+                                                    _dt(x_dtype), _stream(stream)),
+           "rmsnorm_token_logprob_bwd")
+
+
+def rmsnorm_policy_loss_fwd(logits, ld, targets, inv_temperature, old_logp, ref_logp, advantages,
+                            weights, clip_low, clip_high, kl_coef, loss, token_loss, logp, lse,
+                            dlogp, dlogits, ld_out, M, V, x_dtype, stream=None):
+    """Clipped policy loss; dlogits (None to skip) takes its gradient in the same pass."""
+    _check(load_library().rmsnorm_policy_loss_fwd(
+        _ptr(logits), ld, _ptr(targets), inv_temperature, _ptr(old_logp), _ptr(ref_logp),
+        _ptr(advantages), _ptr(weights), clip_low, clip_high, kl_coef, _ptr(loss),
+        _ptr(token_loss), _ptr(logp), _ptr(lse), _ptr(dlogp), _ptr(dlogits), ld_out, M, V,
+        _dt(x_dtype), _stream(stream)), "rmsnorm_policy_loss_fwd")
+
+
+def rmsnorm_preference_loss_fwd(logits, ld, targets, inv_temperature, ref_logp, cu_seqlens, pairs,
+                                beta, label_smoothing, loss, margins, logp, lse, dlogp, M, V,
+                                x_dtype, stream=None):
+    """Preference loss over pairs of sequences (chosen first, then rejected)."""
+    _check(load_library().rmsnorm_preference_loss_fwd(
+        _ptr(logits), ld, _ptr(targets), inv_temperature, _ptr(ref_logp), _ptr(cu_seqlens), pairs,
+        beta, label_smoothing, _ptr(loss), _ptr(margins), _ptr(logp), _ptr(lse), _ptr(dlogp), M,
+        V, _dt(x_dtype), _stream(stream)), "rmsnorm_preference_loss_fwd")
 
 
 def rmsnorm_check_device(stream=None):

@@ -1,8 +1,8 @@
 """Build librmsnorm_gb300.so in-tree with nvcc for sm_103a.
 
-Twenty-eight translation units (forward, backward, staged, ragged, mixed-alignment
-ragged, cluster, wide, quantised-output and LayerNorm kernels once per dtype pair,
-plus the C ABI)
+The translation units (forward, backward, staged, ragged, mixed-alignment ragged,
+cluster, wide, quantised-output, LayerNorm and rotary kernels once per dtype pair,
+the token losses once per logits dtype, plus the C ABI)
 compile in parallel, then link into one shared library with the CUDA runtime
 linked statically.  Rebuilds only when a source is newer than the library.
 """
@@ -51,6 +51,11 @@ UNITS = [("rmsnorm_fwd.cu", ["-DRMSN_PAIR=0"], "fwd_p0.o"),
          ("rmsnorm_wide.cu", ["-DRMSN_PAIR=0"], "wide_p0.o"),
          ("rmsnorm_wide.cu", ["-DRMSN_PAIR=1"], "wide_p1.o"),
          ("rmsnorm_wide.cu", ["-DRMSN_PAIR=2"], "wide_p2.o"),
+         ("rmsnorm_rope.cu", ["-DRMSN_PAIR=0"], "rope_p0.o"),
+         ("rmsnorm_rope.cu", ["-DRMSN_PAIR=1"], "rope_p1.o"),
+         ("rmsnorm_rope.cu", ["-DRMSN_PAIR=2"], "rope_p2.o"),
+         ("rmsnorm_loss.cu", ["-DRMSN_PAIR=0"], "loss_p0.o"),
+         ("rmsnorm_loss.cu", ["-DRMSN_PAIR=1"], "loss_p1.o"),
          ("rmsnorm_api.cu", [], "api.o")]
 
 

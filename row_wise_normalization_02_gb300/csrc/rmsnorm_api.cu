@@ -1595,6 +1595,574 @@ rmsnorm_status_t ln_bwd_impl(const void* dy, const void* x, const float* mean,
   return RMSNORM_OK;
 }
 
+// ---------------------------------------------------------------- rotary positions
+
+RopeKernel rope_kernel(const RopeKey& k) {
+  if (k.xd == kF32 && k.wd == kF32) return get_rope_kernel_f32_f32(k);
+  if (k.xd == kBF16 && k.wd == kBF16) return get_rope_kernel_bf16_bf16(k);
+  if (k.xd == kBF16 && k.wd == kF32) return get_rope_kernel_bf16_f32(k);
+  return nullptr;
+}
+
+constexpr int64_t kRopeMaxT = (int64_t(1) << 30) - 1;
+constexpr int64_t kRopeMaxHeads = 1 << 16;
+static_assert(kRopeMaxAxes == RMSNORM_ROPE_MAX_AXES && kRopeMaxD == RMSNORM_ROPE_MAX_D, "header");
+
+rmsnorm_status_t check_rope_sizes(int64_t T, int64_t hq, int64_t hk, int64_t D) {
+  if (T < 0 || T > kRopeMaxT || D < 1 || D > kRopeMaxD || hq < 0 || hk < 0 ||
+      hq > kRopeMaxHeads || hk > kRopeMaxHeads || hq + hk > kRopeMaxHeads)
+    return RMSNORM_ERR_INVALID_ARG;
+  return RMSNORM_OK;
+}
+
+rmsnorm_status_t check_rope(const rmsnorm_rope_t* r, int64_t T, int64_t D) {
+  if (!r || r->axes < 1 || r->axes > kRopeMaxAxes || r->pairs < 0 || r->pairs > 1 ||
+      r->order < 0 || r->order > 1 || r->rotary_dim < 2 || r->rotary_dim > D ||
+      r->rotary_dim % 2)
+    return RMSNORM_ERR_INVALID_ARG;
+  const int64_t half = r->rotary_dim / 2;
+  int64_t sum = 0;
+  for (int a = 0; a < r->axes; ++a) {
+    const int64_t n = r->sections[a];
+    if (n < 0 || n > half) return RMSNORM_ERR_INVALID_ARG;
+    if (r->order == RMSNORM_ROPE_INTERLEAVED && a > 0 && n > 0 && a + r->axes * (n - 1) >= half)
+      return RMSNORM_ERR_INVALID_ARG;
+    sum += n;
+  }
+  if (sum != half || (r->axes > 1 && r->positions_stride < T)) return RMSNORM_ERR_INVALID_ARG;
+  if (T == 0) return RMSNORM_OK;
+  if (!r->positions || !r->inv_freq) return RMSNORM_ERR_INVALID_ARG;
+  if (!aligned_to(r->positions, 8) || !aligned_to(r->inv_freq, 4)) return RMSNORM_ERR_MISALIGNED;
+  return RMSNORM_OK;
+}
+
+// A view's byte span, or false when its rows overlap or the span does not fit
+// 63 bits.
+bool view_span(const rmsnorm_heads_t& v, int64_t T, int64_t D, int es, size_t* bytes) {
+  *bytes = 0;
+  if (!strided_layout_ok(1, v.heads, D, v.stride_token, v.stride_head)) return false;
+  if (T == 0 || v.heads == 0) return true;
+  int64_t a, b;
+  if (__builtin_mul_overflow(T - 1, v.stride_token, &a) ||
+      __builtin_mul_overflow(v.heads - 1, v.stride_head, &b) || b > (int64_t(1) << 60) ||
+      (T > 1 && v.stride_token < b + D) || __builtin_add_overflow(a, b + D, &a) ||
+      a > (int64_t(1) << 60))
+    return false;
+  *bytes = (size_t)a * (size_t)es;
+  return true;
+}
+
+// An operand of a rotary call: a flat byte range, or the rows of a view.
+struct Span {
+  const void* p;
+  size_t n;                          // bytes from the first element to the last
+  bool written;
+  const rmsnorm_heads_t* view;       // null: flat
+};
+
+// Whether two operands may share a byte.  Views cut out of one buffer side by
+// side (q and k of a fused projection's rows; k and v heads in turn) cover each
+// other's range without sharing a row: with equal token strides their tokens'
+// row ranges, or with equal head strides that divide the token strides their
+// rows, are compared modulo that stride.
+bool spans_overlap(const Span& a, const Span& b, int64_t D, int es) {
+  if (!overlap(a.p, a.n, b.p, b.n)) return false;
+  if (!a.view || !b.view) return true;
+  const rmsnorm_heads_t &u = *a.view, &v = *b.view;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(v.data) -
+                              reinterpret_cast<uintptr_t>(u.data));
+  auto apart = [&](int64_t period, int64_t wu, int64_t wv) {   // bytes
+    if (period <= 0) return false;
+    const int64_t m = ((d % period) + period) % period;
+    return m >= wu && m + wv <= period;
+  };
+  if (u.stride_token == v.stride_token &&
+      apart(u.stride_token * es, ((u.heads - 1) * u.stride_head + D) * es,
+            ((v.heads - 1) * v.stride_head + D) * es))
+    return false;
+  if (u.stride_head == v.stride_head && u.stride_head > 0 &&
+      u.stride_token % u.stride_head == 0 && v.stride_token % u.stride_head == 0 &&
+      apart(u.stride_head * es, D * es, D * es))
+    return false;
+  return true;
+}
+
+bool view_vec_ok(const rmsnorm_heads_t& v, int es) {
+  return aligned_to(v.data, 16) && v.stride_token * es % 16 == 0 && v.stride_head * es % 16 == 0;
+}
+
+// Lanes per row for D elements as two vectors per lane, or 0 (scalar kernel).
+int rope_lanes(int64_t D, int64_t R, int xd, bool views_ok) {
+  const int64_t pair = 2 * per_vec(xd);
+  if (!views_ok || D % pair || R % pair || D > 32 * pair) return 0;
+  int g = 4;
+  while (g * pair < D) g *= 2;
+  return g;
+}
+
+// Work items: a token's rows in chunks, so many that small batches spread over
+// the SMs (kRopeItems of them when the rows allow), each of whole steps of
+// `step` rows.
+constexpr int64_t kRopeItems = 4096;
+void rope_chunks(int64_t T, int rows, int step, int* chunks, int* per_chunk) {
+  const int64_t steps = (rows + step - 1) / step;
+  int64_t c = T > 0 ? (kRopeItems + T - 1) / T : 1;
+  if (c > steps) c = steps;
+  if (c < 1) c = 1;
+  *per_chunk = (int)((steps + c - 1) / c) * step;
+  *chunks = *per_chunk > 0 ? (rows + *per_chunk - 1) / *per_chunk : 1;
+  if (*chunks < 1) *chunks = 1;
+}
+
+// Resident CTAs per SM that the normed backward runs and its workspace allows
+// for: the vectorised kernel is built for two, the scalar one (threads of a few
+// warps for short rows) takes more of them.
+int rope_bwd_cap(int sms, int64_t D) { return sms * (D <= 512 ? 8 : 2); }
+size_t rope_bwd_bytes(int64_t cap, int64_t D) {
+  return (size_t)cap * 2 * (size_t)round_up((int)D, 4) * 4;
+}
+int64_t rope_bwd_ctas(int sms, int64_t T, int64_t heads, int64_t D) {
+  const int64_t cap = rope_bwd_cap(sms, D);
+  return T * heads < cap ? T * heads : cap;
+}
+
+rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_heads_t* k,
+                           const rmsnorm_heads_t* dq, const rmsnorm_heads_t* dk,
+                           const void* q_gamma, const void* k_gamma,
+                           const rmsnorm_heads_t* q_out, const rmsnorm_heads_t* k_out,
+                           float* dq_gamma, float* dk_gamma, void* workspace,
+                           size_t workspace_bytes, const rmsnorm_rope_t* rope, int64_t T,
+                           int64_t D, float eps, int xd, int wd, cudaStream_t stream) {
+  // what this call reads per view: x (absent in the rotation's own backward),
+  // dy (backward); what it writes: out.  lead[i] is the view both sizes come from.
+  const bool norm = q_gamma != nullptr;
+  const rmsnorm_heads_t* x[2] = {q, k};
+  const rmsnorm_heads_t* dy[2] = {dq, dk};
+  const rmsnorm_heads_t* out[2] = {q_out, k_out};
+  const void* gamma[2] = {q_gamma, k_gamma};
+  float* dgamma[2] = {dq_gamma, dk_gamma};
+  if (!norm) wd = xd;
+  if (!dtype_pair_ok(xd, wd)) return RMSNORM_ERR_UNSUPPORTED_DTYPE;
+  if (norm && (!(eps >= 0.f) || isinf(eps))) return RMSNORM_ERR_INVALID_ARG;
+  const rmsnorm_heads_t** lead = bwd ? dy : x;
+  if (!lead[0] || !out[0]) return RMSNORM_ERR_INVALID_ARG;
+  const bool has_k = lead[1] != nullptr;
+  if (has_k ? !out[1] || (k_gamma != nullptr) != norm
+            : out[1] || k_gamma || dk_gamma || (bwd && x[1]))
+    return RMSNORM_ERR_INVALID_ARG;
+  if (!norm && (dq_gamma || dk_gamma)) return RMSNORM_ERR_INVALID_ARG;
+  const int64_t heads[2] = {lead[0]->heads, has_k ? lead[1]->heads : 0};
+  rmsnorm_status_t st = check_rope_sizes(T, heads[0], heads[1], D);
+  if (st != RMSNORM_OK) return st;
+  if ((st = check_rope(rope, T, D)) != RMSNORM_OK) return st;
+
+  const int es = esize(xd);
+  Span spans[16];
+  int ns = 0;   // at most 3 views, gamma and dgamma per side, 2 of the rotation, the workspace
+  bool views_ok = true;
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    const rmsnorm_heads_t* views[3] = {!bwd || norm ? x[i] : nullptr, bwd ? dy[i] : nullptr,
+                                       out[i]};
+    const bool need[3] = {!bwd || norm, bwd, true};
+    for (int j = 0; j < 3; ++j) {
+      if (!need[j]) continue;
+      const rmsnorm_heads_t* v = views[j];
+      size_t n;
+      if (!v || v->heads != heads[i] || !view_span(*v, T, D, es, &n))
+        return RMSNORM_ERR_INVALID_ARG;
+      if (T > 0 && !v->data) return RMSNORM_ERR_INVALID_ARG;
+      if (T > 0 && !aligned_to(v->data, (size_t)es)) return RMSNORM_ERR_MISALIGNED;
+      views_ok = views_ok && view_vec_ok(*v, es);
+      // in place: the output over the view it replaces, with its strides
+      const rmsnorm_heads_t* from = bwd ? dy[i] : x[i];
+      const bool in_place = j == 2 && v->data == from->data &&
+                            v->stride_token == from->stride_token &&
+                            v->stride_head == from->stride_head;
+      if (!in_place) spans[ns++] = Span{v->data, n, j == 2, v};
+      else spans[ns - 1].written = true;   // `from` is the view added just before
+    }
+    if (norm) {
+      if (!aligned_to(gamma[i], (size_t)esize(wd)) ||
+          (dgamma[i] && !aligned_to(dgamma[i], 4)))
+        return RMSNORM_ERR_MISALIGNED;
+      views_ok = views_ok && aligned_to(gamma[i], 16);
+      spans[ns++] = Span{gamma[i], (size_t)D * esize(wd), false, nullptr};
+      if (dgamma[i]) spans[ns++] = Span{dgamma[i], (size_t)D * 4, true, nullptr};
+    }
+  }
+  const bool sums = dq_gamma || dk_gamma;
+  if (T == 0 || heads[0] + heads[1] == 0) {
+    for (int i = 0; i < 2; ++i)
+      if (dgamma[i]) {
+        const cudaError_t e = cudaMemsetAsync(dgamma[i], 0, (size_t)D * 4, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync of a weight gradient");
+      }
+    return RMSNORM_OK;
+  }
+  spans[ns++] = Span{rope->positions, (size_t)((rope->axes - 1) * rope->positions_stride + T) * 8,
+                     false, nullptr};
+  spans[ns++] = Span{rope->inv_freq, (size_t)rope->rotary_dim * 2, false, nullptr};
+  int dev;
+  DevInfo di;
+  if (sums && (!workspace || !aligned_to(workspace, 16))) return RMSNORM_ERR_WORKSPACE;
+  auto overlaps = [&]() {
+    for (int i = 0; i < ns; ++i)
+      for (int j = i + 1; j < ns; ++j)
+        if ((spans[i].written || spans[j].written) &&
+            spans_overlap(spans[i], spans[j], D, es))
+          return true;
+    return false;
+  };
+  if (overlaps()) return RMSNORM_ERR_INVALID_ARG;
+  if ((st = current_device(&dev)) != RMSNORM_OK) return st;
+  cudaError_t e = device_info(dev, &di);
+  if (e != cudaSuccess) return cuda_fail(e, "device attributes");
+  const int64_t ctas = rope_bwd_ctas(di.sms, T, heads[0] + heads[1], D);
+  if (sums) {
+    const size_t need = rope_bwd_bytes(ctas, D);
+    if (workspace_bytes < need) return RMSNORM_ERR_WORKSPACE;
+    spans[ns++] = Span{workspace, need, true, nullptr};
+    if (overlaps()) return RMSNORM_ERR_INVALID_ARG;
+  }
+
+  const int64_t R = rope->rotary_dim;
+  const bool norm_bwd = bwd && norm;
+  const int g = rope_lanes(D, R, xd, views_ok);
+  const RopeKernel fn = rope_kernel(RopeKey{xd, wd, norm_bwd, norm, rope->pairs == 1, g});
+  if (!fn) return RMSNORM_ERR_INVALID_ARG;
+
+  RopeParams p = {};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    const rmsnorm_heads_t* in = norm_bwd || !bwd ? x[i] : dy[i];
+    p.v[i].x = in->data;
+    p.v[i].x_st = in->stride_token;
+    p.v[i].x_sh = in->stride_head;
+    if (norm_bwd) {
+      p.v[i].dy = dy[i]->data;
+      p.v[i].dy_st = dy[i]->stride_token;
+      p.v[i].dy_sh = dy[i]->stride_head;
+    }
+    p.v[i].y = out[i]->data;
+    p.v[i].y_st = out[i]->stride_token;
+    p.v[i].y_sh = out[i]->stride_head;
+    p.v[i].gamma = gamma[i];
+    p.v[i].heads = (int)heads[i];
+  }
+  p.positions = rope->positions;
+  p.pos_st = rope->positions_stride;
+  p.inv_freq = rope->inv_freq;
+  p.axes = rope->axes;
+  p.order = rope->order;
+  for (int a = 0; a < rope->axes; ++a) p.sections[a] = rope->sections[a];
+  p.T = T;
+  p.D = (int)D;
+  p.R = (int)R;
+  p.sign = bwd ? -1.f : 1.f;
+  p.eps = eps;
+  p.inv_d = 1.0f / (float)D;
+  p.ld_half = round_up((int)D, 4);
+  p.partial = sums ? static_cast<float*>(workspace) : nullptr;
+
+  const int angles = (int)(R / 2 + 1) / 2 * 2 * 8;   // one token's table, bytes
+  int64_t grid;
+  int threads = kRopeThreads, smem;
+  if (g > 0) {
+    const int step = 32 / g, warps = kRopeThreads / 32;
+    smem = warps * angles + (norm_bwd ? warps * (int)D * 4 : 0);
+    if (!norm_bwd) {
+      rope_chunks(T, (int)(heads[0] + heads[1]), step, &p.chunks[0], &p.heads_per_chunk[0]);
+      grid = (T * p.chunks[0] + warps - 1) / warps;
+    } else {
+      int64_t items = 0;
+      for (int i = 0; i < 2; ++i) {
+        rope_chunks(T, (int)heads[i], step, &p.chunks[i], &p.heads_per_chunk[i]);
+        if (heads[i]) items += T * p.chunks[i];
+      }
+      grid = (items + warps - 1) / warps;
+      if (grid > 2 * di.sms) grid = 2 * di.sms;
+      if (grid > ctas) grid = ctas;
+    }
+  } else {
+    const int64_t steps = D - R / 2;   // columns or pairs a row's threads share
+    threads = steps >= kRopeThreads ? kRopeThreads : round_up((int)steps, 32);
+    smem = (int)R * 4 + (norm_bwd ? (int)D * 4 : 0);
+    int64_t items = 0;
+    for (int i = 0; i < 2; ++i) {
+      rope_chunks(T, (int)heads[i], 1, &p.chunks[i], &p.heads_per_chunk[i]);
+      if (heads[i]) items += T * p.chunks[i];
+    }
+    const int64_t cap = norm_bwd ? ctas : (int64_t)di.sms * 32;
+    grid = items < cap ? items : cap;
+  }
+  if ((e = ensure_smem(reinterpret_cast<const void*>(fn), dev, smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, "shared memory of the rotary kernel");
+  }
+  e = launch(fn, (int)grid, threads, smem, stream, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, bwd ? "rotary backward launch" : "rotary forward launch");
+  }
+  if (!sums) return RMSNORM_OK;
+  e = launch_colsum(p.partial, (int)grid, 2 * p.ld_half / 4,
+                    ColSumOut{dq_gamma, dk_gamma, p.ld_half / 4, (int)D, 0}, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, "rotary backward stage-2 launch");
+  }
+  return RMSNORM_OK;
+}
+
+// ---------------------------------------------------------------- token losses
+
+constexpr int64_t kLossMaxM = (int64_t(1) << 28) - 1;
+
+// Operands of a loss call, checked for NULL, alignment and overlap as they are
+// listed.
+struct LossOperands {
+  struct One {
+    const void* p;
+    size_t n;
+    bool written;
+  };
+  One v[16];
+  int n = 0;
+  rmsnorm_status_t st = RMSNORM_OK;
+
+  // `align`-aligned operand of `bytes`; optional ones may be NULL
+  void add(const void* p, size_t bytes, size_t align, bool written, bool optional = false) {
+    if (st != RMSNORM_OK || bytes == 0) return;
+    if (!p) {
+      if (!optional) st = RMSNORM_ERR_INVALID_ARG;
+      return;
+    }
+    if (!aligned_to(p, align)) {
+      st = RMSNORM_ERR_MISALIGNED;
+      return;
+    }
+    v[n++] = One{p, bytes, written};
+  }
+  rmsnorm_status_t check() const {
+    for (int i = 0; i < n && st == RMSNORM_OK; ++i)
+      for (int j = i + 1; j < n; ++j)
+        if ((v[i].written || v[j].written) && overlap(v[i].p, v[i].n, v[j].p, v[j].n))
+          return RMSNORM_ERR_INVALID_ARG;
+    return st;
+  }
+};
+
+// M rows of V with row stride ld, in bytes; 0 with a bad stride reported.
+size_t rows_span(int64_t M, int64_t V, int64_t ld, int es, rmsnorm_status_t* st) {
+  int64_t n;
+  if (M > 1 && ld < V) *st = RMSNORM_ERR_INVALID_ARG;
+  if (M == 0 || *st != RMSNORM_OK) return 0;
+  if (__builtin_mul_overflow(M - 1, ld, &n) || n < 0 || n > (int64_t(1) << 60)) {
+    *st = RMSNORM_ERR_INVALID_ARG;
+    return 0;
+  }
+  return (size_t)(n + V) * es;
+}
+
+rmsnorm_status_t check_loss(int64_t M, int64_t V, double inv_t, int xd) {
+  if (M < 0 || M > kLossMaxM || V < 1 || V > kMaxN || !(inv_t > 0.0) || !isfinite(inv_t) ||
+      !isfinite((float)inv_t * 1.5f) || !((float)inv_t > 0.f))
+    return RMSNORM_ERR_INVALID_ARG;
+  if (xd != kF32 && xd != kBF16) return RMSNORM_ERR_UNSUPPORTED_DTYPE;
+  return RMSNORM_OK;
+}
+
+LossParams loss_params(const void* logits, int64_t ld, const int64_t* targets, double inv_t,
+                       int64_t M, int64_t V) {
+  LossParams p = {};
+  p.logits = logits;
+  p.ld = ld;
+  p.targets = targets;
+  p.M = M;
+  p.V = (int)V;
+  p.inv_t = inv_t;
+  p.inv_tf = (float)inv_t;
+  p.c1 = (float)(inv_t * 1.4426950408889634);
+  return p;
+}
+
+// Adds the dlogits operand (in place over the logits is the one overlap
+// allowed), the logits and their span.
+void add_logits(LossOperands* ops, const void* logits, int64_t ld, void* dlogits, int64_t ld_out,
+                int64_t M, int64_t V, int xd, bool want) {
+  const int es = esize(xd);
+  const size_t in = rows_span(M, V, ld, es, &ops->st);
+  const bool in_place = want && dlogits == logits && ld_out == ld;
+  ops->add(logits, in, (size_t)es, in_place);
+  if (!want) return;
+  const size_t out = rows_span(M, V, ld_out, es, &ops->st);
+  if (!in_place) ops->add(dlogits, out, (size_t)es, true);
+}
+
+// The row kernel: a CTA per row, or clusters of up to eight per row while the
+// SMs would not have two CTAs each and a CTA keeps a batch of vectors.
+rmsnorm_status_t launch_loss_rows(int mode, int xd, const LossParams& p, cudaStream_t stream) {
+  int dev;
+  rmsnorm_status_t st = current_device(&dev);
+  if (st != RMSNORM_OK) return st;
+  DevInfo di;
+  cudaError_t e = device_info(dev, &di);
+  if (e != cudaSuccess) return cuda_fail(e, "device attributes");
+  const int64_t nvec = p.V / per_vec(xd);
+  int cl = 1;
+  while (cl < 8 && p.M * cl * 2 <= 2 * di.sms && nvec / (2 * cl) >= kLossThreads) cl *= 2;
+  int threads = (int)((nvec / cl + kLossBatch - 1) / kLossBatch);
+  threads = threads >= kLossThreads ? kLossThreads : round_up(threads < 64 ? 64 : threads, 32);
+  const LossKernel fn = xd == kF32 ? get_loss_row_f32(mode, cl) : get_loss_row_bf16(mode, cl);
+  e = launch_in_clusters(cl > 1 ? cl : 0, fn, (int)(p.M * cl), threads, 0, stream, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, "token log-probability launch");
+  }
+  return RMSNORM_OK;
+}
+
+rmsnorm_status_t launch_loss(LossKernel fn, int64_t grid, int threads, const LossParams& p,
+                             cudaStream_t stream, const char* what) {
+  const cudaError_t e = launch(fn, (int)grid, threads, 0, stream, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, what);
+  }
+  return RMSNORM_OK;
+}
+
+rmsnorm_status_t token_logprob_fwd_impl(const void* logits, int64_t ld, const int64_t* targets,
+                                        double inv_t, float* logp, float* lse, int64_t M,
+                                        int64_t V, int xd, cudaStream_t stream) {
+  rmsnorm_status_t st = check_loss(M, V, inv_t, xd);
+  if (st != RMSNORM_OK) return st;
+  if (M == 0) return RMSNORM_OK;
+  LossOperands ops;
+  add_logits(&ops, logits, ld, nullptr, 0, M, V, xd, false);
+  const size_t rows = (size_t)M * 4;
+  ops.add(targets, rows * 2, 8, false);
+  ops.add(logp, rows, 4, true);
+  ops.add(lse, rows, 4, true);
+  if ((st = ops.check()) != RMSNORM_OK) return st;
+  LossParams p = loss_params(logits, ld, targets, inv_t, M, V);
+  p.logp = logp;
+  p.lse = lse;
+  return launch_loss_rows(kLossLogprob, xd, p, stream);
+}
+
+rmsnorm_status_t token_logprob_bwd_impl(const void* logits, int64_t ld, const int64_t* targets,
+                                        double inv_t, const float* lse, const float* dlogp,
+                                        const float* scale, void* dlogits, int64_t ld_out,
+                                        int64_t M, int64_t V, int xd, cudaStream_t stream) {
+  rmsnorm_status_t st = check_loss(M, V, inv_t, xd);
+  if (st != RMSNORM_OK) return st;
+  if (M == 0) return RMSNORM_OK;
+  LossOperands ops;
+  add_logits(&ops, logits, ld, dlogits, ld_out, M, V, xd, true);
+  const size_t rows = (size_t)M * 4;
+  ops.add(targets, rows * 2, 8, false);
+  ops.add(lse, rows, 4, false);
+  ops.add(dlogp, rows, 4, false);
+  ops.add(scale, 4, 4, false, true);
+  if ((st = ops.check()) != RMSNORM_OK) return st;
+  LossParams p = loss_params(logits, ld, targets, inv_t, M, V);
+  p.lse = const_cast<float*>(lse);
+  p.dlogp_in = dlogp;
+  p.scale = scale;
+  p.dlogits = dlogits;
+  p.ld_out = ld_out;
+  const int64_t per = (int64_t)kLossBwdVecs * per_vec(xd);
+  const int64_t items = M * ((V + per - 1) / per), cap = int64_t(1) << 30;
+  return launch_loss(xd == kF32 ? get_loss_bwd_f32() : get_loss_bwd_bf16(),
+                     items < cap ? items : cap, kLossThreads, p, stream,
+                     "logits gradient launch");
+}
+
+rmsnorm_status_t policy_loss_impl(const void* logits, int64_t ld, const int64_t* targets,
+                                  double inv_t, const float* old_logp, const float* ref_logp,
+                                  const float* advantages, const float* weights, float clip_low,
+                                  float clip_high, float kl_coef, float* loss, float* token_loss,
+                                  float* logp, float* lse, float* dlogp, void* dlogits,
+                                  int64_t ld_out, int64_t M, int64_t V, int xd,
+                                  cudaStream_t stream) {
+  rmsnorm_status_t st = check_loss(M, V, inv_t, xd);
+  if (st != RMSNORM_OK) return st;
+  if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f) || isinf(clip_high) ||
+      (ref_logp && (!(kl_coef >= 0.f) || isinf(kl_coef))))
+    return RMSNORM_ERR_INVALID_ARG;
+  LossOperands ops;
+  const size_t rows = (size_t)M * 4;
+  add_logits(&ops, logits, ld, dlogits, ld_out, M, V, xd, dlogits != nullptr);
+  ops.add(targets, rows * 2, 8, false);
+  ops.add(old_logp, rows, 4, false);
+  ops.add(ref_logp, rows, 4, false, true);
+  ops.add(advantages, rows, 4, false);
+  ops.add(weights, rows, 4, false, true);
+  ops.add(loss, 4, 4, true);
+  for (float* out : {token_loss, logp, lse, dlogp}) ops.add(out, rows, 4, true);
+  if ((st = ops.check()) != RMSNORM_OK) return st;
+  LossParams p = loss_params(logits, ld, targets, inv_t, M, V);
+  p.logp = logp;
+  p.lse = lse;
+  p.dlogp = dlogp;
+  p.old_logp = old_logp;
+  p.ref_logp = ref_logp;
+  p.advantages = advantages;
+  p.weights = weights;
+  p.ratio_lo = 1.f - clip_low;
+  p.ratio_hi = 1.f + clip_high;
+  p.kl = kl_coef;
+  p.token_loss = token_loss;
+  p.loss = loss;
+  p.dlogits = dlogits;
+  p.ld_out = ld_out;
+  if (M > 0 &&
+      (st = launch_loss_rows(dlogits ? kLossPolicyGrad : kLossPolicy, xd, p, stream)) !=
+          RMSNORM_OK)
+    return st;
+  return launch_loss(get_loss_sum(), 1, 1024, p, stream, "loss sum launch");
+}
+
+rmsnorm_status_t preference_loss_impl(const void* logits, int64_t ld, const int64_t* targets,
+                                      double inv_t, const float* ref_logp, const int64_t* cu,
+                                      int64_t pairs, float beta, float smoothing, float* loss,
+                                      float* margins, float* logp, float* lse, float* dlogp,
+                                      int64_t M, int64_t V, int xd, cudaStream_t stream) {
+  rmsnorm_status_t st = check_loss(M, V, inv_t, xd);
+  if (st != RMSNORM_OK) return st;
+  if (pairs < 1 || pairs >= (int64_t(1) << 24) || !isfinite(beta) ||
+      !(smoothing >= 0.f && smoothing <= 1.f))
+    return RMSNORM_ERR_INVALID_ARG;
+  LossOperands ops;
+  const size_t rows = (size_t)M * 4;
+  add_logits(&ops, logits, ld, nullptr, 0, M, V, xd, false);
+  ops.add(targets, rows * 2, 8, false);
+  ops.add(ref_logp, rows, 4, false, true);
+  ops.add(cu, (size_t)(2 * pairs + 1) * 8, 8, false);
+  ops.add(loss, 4, 4, true);
+  ops.add(margins, (size_t)pairs * 4, 4, true);
+  for (float* out : {logp, lse, dlogp}) ops.add(out, rows, 4, true);
+  if ((st = ops.check()) != RMSNORM_OK) return st;
+  LossParams p = loss_params(logits, ld, targets, inv_t, M, V);
+  p.logp = logp;
+  p.lse = lse;
+  p.dlogp = dlogp;
+  p.ref_logp = ref_logp;
+  p.cu = cu;
+  p.pairs = pairs;
+  p.beta = beta;
+  p.smoothing = smoothing;
+  p.margins = margins;
+  p.loss = loss;
+  if (M > 0 && (st = launch_loss_rows(kLossPreference, xd, p, stream)) != RMSNORM_OK) return st;
+  if ((st = launch_loss(get_loss_pairs(), pairs, kLossThreads, p, stream,
+                        "preference margins launch")) != RMSNORM_OK)
+    return st;
+  return launch_loss(get_loss_pairs_mean(), 1, kLossThreads, p, stream, "preference loss launch");
+}
+
 // ---------------------------------------------------------------- backward
 
 // Stage-1 CTA count bound for these sizes: the grid of the plan for 16-byte
@@ -1913,6 +2481,90 @@ rmsnorm_status_t rmsnorm_bwd_noalloc(const void* dy, const void* x, const float*
   return bwd_impl(dy, x, rstd, gamma, dx, nullptr, dgamma, false, scratch,
                   scratch ? (size_t)RMSNORM_BWD_NOALLOC_SCRATCH_BYTES : 0, M, N, eps,
                   (int)x_dtype, (int)w_dtype, stream, true);
+}
+
+rmsnorm_status_t rmsnorm_rope_fwd(const rmsnorm_heads_t* q, const rmsnorm_heads_t* k,
+                                  const void* q_gamma, const void* k_gamma,
+                                  const rmsnorm_heads_t* q_out, const rmsnorm_heads_t* k_out,
+                                  const rmsnorm_rope_t* rope, int64_t T, int64_t D, float eps,
+                                  rmsnorm_dtype_t x_dtype, rmsnorm_dtype_t w_dtype,
+                                  cudaStream_t stream) {
+  return rope_impl(false, q, k, nullptr, nullptr, q_gamma, k_gamma, q_out, k_out, nullptr,
+                   nullptr, nullptr, 0, rope, T, D, eps, (int)x_dtype, (int)w_dtype, stream);
+}
+
+rmsnorm_status_t rmsnorm_rope_bwd_workspace_size(int64_t T, int64_t q_heads, int64_t k_heads,
+                                                 int64_t D, rmsnorm_dtype_t x_dtype,
+                                                 rmsnorm_dtype_t w_dtype, int device,
+                                                 size_t* bytes) {
+  if (!bytes) return RMSNORM_ERR_INVALID_ARG;
+  *bytes = 0;
+  rmsnorm_status_t st = check_rope_sizes(T, q_heads, k_heads, D);
+  if (st != RMSNORM_OK) return st;
+  if (!dtype_pair_ok((int)x_dtype, (int)w_dtype)) return RMSNORM_ERR_UNSUPPORTED_DTYPE;
+  if (T == 0 || q_heads + k_heads == 0) return RMSNORM_OK;
+  if (device < 0 && (st = current_device(&device)) != RMSNORM_OK) return st;
+  DevInfo di;
+  const cudaError_t e = device_info(device, &di);
+  if (e != cudaSuccess) return cuda_fail(e, "device attributes");
+  *bytes = rope_bwd_bytes(rope_bwd_ctas(di.sms, T, q_heads + k_heads, D), D);
+  return RMSNORM_OK;
+}
+
+rmsnorm_status_t rmsnorm_rope_bwd(const rmsnorm_heads_t* dq_out, const rmsnorm_heads_t* dk_out,
+                                  const rmsnorm_heads_t* q, const rmsnorm_heads_t* k,
+                                  const void* q_gamma, const void* k_gamma,
+                                  const rmsnorm_heads_t* dq, const rmsnorm_heads_t* dk,
+                                  float* dq_gamma, float* dk_gamma, void* workspace,
+                                  size_t workspace_bytes, const rmsnorm_rope_t* rope, int64_t T,
+                                  int64_t D, float eps, rmsnorm_dtype_t x_dtype,
+                                  rmsnorm_dtype_t w_dtype, cudaStream_t stream) {
+  return rope_impl(true, q, k, dq_out, dk_out, q_gamma, k_gamma, dq, dk, dq_gamma, dk_gamma,
+                   workspace, workspace_bytes, rope, T, D, eps, (int)x_dtype, (int)w_dtype,
+                   stream);
+}
+
+rmsnorm_status_t rmsnorm_token_logprob_fwd(const void* logits, int64_t ld,
+                                           const int64_t* targets, double inv_temperature,
+                                           float* logp, float* lse, int64_t M, int64_t V,
+                                           rmsnorm_dtype_t x_dtype, cudaStream_t stream) {
+  return token_logprob_fwd_impl(logits, ld, targets, inv_temperature, logp, lse, M, V,
+                                (int)x_dtype, stream);
+}
+
+rmsnorm_status_t rmsnorm_token_logprob_bwd(const void* logits, int64_t ld,
+                                           const int64_t* targets, double inv_temperature,
+                                           const float* lse, const float* dlogp,
+                                           const float* scale, void* dlogits, int64_t ld_out,
+                                           int64_t M, int64_t V, rmsnorm_dtype_t x_dtype,
+                                           cudaStream_t stream) {
+  return token_logprob_bwd_impl(logits, ld, targets, inv_temperature, lse, dlogp, scale, dlogits,
+                                ld_out, M, V, (int)x_dtype, stream);
+}
+
+rmsnorm_status_t rmsnorm_policy_loss_fwd(const void* logits, int64_t ld, const int64_t* targets,
+                                         double inv_temperature, const float* old_logp,
+                                         const float* ref_logp, const float* advantages,
+                                         const float* weights, float clip_low, float clip_high,
+                                         float kl_coef, float* loss, float* token_loss,
+                                         float* logp, float* lse, float* dlogp, void* dlogits,
+                                         int64_t ld_out, int64_t M, int64_t V,
+                                         rmsnorm_dtype_t x_dtype, cudaStream_t stream) {
+  return policy_loss_impl(logits, ld, targets, inv_temperature, old_logp, ref_logp, advantages,
+                          weights, clip_low, clip_high, kl_coef, loss, token_loss, logp, lse,
+                          dlogp, dlogits, ld_out, M, V, (int)x_dtype, stream);
+}
+
+rmsnorm_status_t rmsnorm_preference_loss_fwd(const void* logits, int64_t ld,
+                                             const int64_t* targets, double inv_temperature,
+                                             const float* ref_logp, const int64_t* cu_seqlens,
+                                             int64_t pairs, float beta, float label_smoothing,
+                                             float* loss, float* margins, float* logp, float* lse,
+                                             float* dlogp, int64_t M, int64_t V,
+                                             rmsnorm_dtype_t x_dtype, cudaStream_t stream) {
+  return preference_loss_impl(logits, ld, targets, inv_temperature, ref_logp, cu_seqlens, pairs,
+                              beta, label_smoothing, loss, margins, logp, lse, dlogp, M, V,
+                              (int)x_dtype, stream);
 }
 
 rmsnorm_status_t rmsnorm_check_device(cudaStream_t stream) {
