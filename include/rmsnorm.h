@@ -405,38 +405,43 @@ rmsnorm_status_t rmsnorm_rope_bwd(const rmsnorm_heads_t* dq_out, const rmsnorm_h
 
 /*
  * Log-probability of each row's target token, the step from a model's logits
- * to the losses below.  With z = logits * inv_temperature (inv_temperature
- * finite and > 0):
- *     lse_i = log sum_j exp(z_ij),     logp_i = z_i,target(i) - lse_i
+ * to the losses below.  With z = logits * inv_temperature (inv_temperature in
+ * [1e-9, 1e9]) and t the row's target:
+ *     logp_i    = z_it - log sum_j exp(z_ij)
+ *     rel_lse_i = log sum_j exp(z_ij - z_it) = -logp_i
+ * the second, the row's log-sum-exp seen from its target, being what the
+ * backward takes: the plain log-sum-exp, rounded at 2^-24 of its size, would
+ * leave that error in every gradient of a confident row.
  * logits: M rows of V elements (x_dtype), row i at logits + i * ld (ld >= V
- * when M > 1; rows need not start on 16 bytes); targets: M int64; logp, lse: M
- * fp32 each.  A negative target leaves its row out: it is not read, logp and
- * lse are 0, and its gradient is zero.  A target >= V gives NaN (in logp, in
- * the losses and in the row's gradient).  Sums are fp32 over values scaled by
- * the row's maximum; lse and logp are put together in 64 bits and rounded once.
- * Logits of -inf have probability 0; a row of nothing else, or with a NaN or
- * +inf, gives NaN.  M < 2^28.  No workspace.
+ * when M > 1; rows need not start on 16 bytes); targets: M int64; logp,
+ * rel_lse: M fp32 each.  A negative target leaves its row out: it is not read,
+ * logp and rel_lse are 0, and its gradient is zero.  A target >= V gives NaN
+ * (in logp, in the losses and in the row's gradient).  Sums are fp32 over
+ * values scaled by the row's maximum; logp is put together in two fp32 parts and
+ * rounded once.  Logits of -inf have probability 0; a row of nothing else, or
+ * with a NaN or +inf, gives NaN.  M < 2^28.  No workspace.
  */
 rmsnorm_status_t rmsnorm_token_logprob_fwd(const void* logits, int64_t ld,
                                            const int64_t* targets, double inv_temperature,
-                                           float* logp, float* lse, int64_t M, int64_t V,
+                                           float* logp, float* rel_lse, int64_t M, int64_t V,
                                            rmsnorm_dtype_t x_dtype, cudaStream_t stream);
 
 /*
  * Gradient of the logits from the gradient of logp -- the backward of
  * rmsnorm_token_logprob_fwd, rmsnorm_policy_loss_fwd and
  * rmsnorm_preference_loss_fwd:
- *     dlogits_ij = scale * dlogp_i * inv_temperature * ([j = target(i)] - exp(z_ij - lse_i))
- * lse: the forward's; dlogp: M fp32 (the losses' forwards write it); scale: one
- * fp32 on the device (the loss's own upstream gradient), or NULL for 1.
+ *     dlogits_ij = scale * dlogp_i * inv_temperature * ([j = t] - exp(z_ij - z_it - rel_lse_i))
+ * rel_lse: the forward's; dlogp: M fp32 (the losses' forwards write it); scale:
+ * one fp32 on the device (the loss's own upstream gradient), or NULL for 1.
  * dlogits: M rows of V (x_dtype), row stride ld_out; it may be logits itself
- * with ld_out = ld (in place).  Rows that are left out, and rows whose dlogp or
- * scale is 0, are set to zero without being read.  A row whose start differs
- * from its logits' modulo 16 bytes takes a scalar path.
+ * with ld_out = ld (in place; a CTA then takes whole rows, which for few long
+ * rows is slower).  Rows that are left out, and rows whose dlogp or scale is 0,
+ * are set to zero without being read.  A row whose start differs from its
+ * logits' modulo 16 bytes takes a scalar path.
  */
 rmsnorm_status_t rmsnorm_token_logprob_bwd(const void* logits, int64_t ld,
                                            const int64_t* targets, double inv_temperature,
-                                           const float* lse, const float* dlogp,
+                                           const float* rel_lse, const float* dlogp,
                                            const float* scale, void* dlogits, int64_t ld_out,
                                            int64_t M, int64_t V, rmsnorm_dtype_t x_dtype,
                                            cudaStream_t stream);
@@ -454,7 +459,7 @@ rmsnorm_status_t rmsnorm_token_logprob_bwd(const void* logits, int64_t ld,
  * live tokens is weights of 1 / their number; a row of weight 0 is worth 0 even
  * where its other values are not finite); ref_logp: M fp32, or NULL for no KL term (kl_coef is
  * then not used).  clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, all finite.
- * loss: one fp32; token_loss, logp, lse, dlogp: M fp32 each.  dlogits: M rows
+ * loss: one fp32; token_loss, logp, rel_lse, dlogp: M fp32 each.  dlogits: M rows
  * of V (x_dtype, row stride ld_out; logits itself with ld_out = ld for in
  * place) for the gradient of loss in the same pass -- each row of logits is
  * read from memory once and written once -- or NULL; the gradient for another
@@ -466,7 +471,7 @@ rmsnorm_status_t rmsnorm_policy_loss_fwd(const void* logits, int64_t ld, const i
                                          const float* ref_logp, const float* advantages,
                                          const float* weights, float clip_low, float clip_high,
                                          float kl_coef, float* loss, float* token_loss,
-                                         float* logp, float* lse, float* dlogp, void* dlogits,
+                                         float* logp, float* rel_lse, float* dlogp, void* dlogits,
                                          int64_t ld_out, int64_t M, int64_t V,
                                          rmsnorm_dtype_t x_dtype, cudaStream_t stream);
 
@@ -484,15 +489,15 @@ rmsnorm_status_t rmsnorm_policy_loss_fwd(const void* logits, int64_t ld, const i
  * on the device, not decreasing, within [0, M] (offsets outside are cut to the
  * batch); an empty sequence has S = 0.  S and the margins are summed in 64 bits.
  * 1 <= pairs < 2^24, beta finite, 0 <= label_smoothing <= 1.  loss: one fp32;
- * margins: `pairs` fp32; logp, lse, dlogp: M fp32 each.  The gradient of the
+ * margins: `pairs` fp32; logp, rel_lse, dlogp: M fp32 each.  The gradient of the
  * logits comes from rmsnorm_token_logprob_bwd.
  */
 rmsnorm_status_t rmsnorm_preference_loss_fwd(const void* logits, int64_t ld,
                                              const int64_t* targets, double inv_temperature,
                                              const float* ref_logp, const int64_t* cu_seqlens,
                                              int64_t pairs, float beta, float label_smoothing,
-                                             float* loss, float* margins, float* logp, float* lse,
-                                             float* dlogp, int64_t M, int64_t V,
+                                             float* loss, float* margins, float* logp,
+                                             float* rel_lse, float* dlogp, int64_t M, int64_t V,
                                              rmsnorm_dtype_t x_dtype, cudaStream_t stream);
 
 /*

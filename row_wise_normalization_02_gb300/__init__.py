@@ -68,6 +68,8 @@ def library_path() -> str:
 def load_library():
     """Load the shared library (raises if it is missing: no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -350,43 +352,44 @@ def rmsnorm_rope_bwd(dq_out, dk_out, q, k, q_gamma, k_gamma, dq, dk, dq_gamma, d
            "rmsnorm_rope_bwd")
 
 
-def rmsnorm_token_logprob_fwd(logits, ld, targets, inv_temperature, logp, lse, M, V, x_dtype,
+def rmsnorm_token_logprob_fwd(logits, ld, targets, inv_temperature, logp, rel_lse, M, V, x_dtype,
                               stream=None):
-    """logp and lse of each row's target token (rows of V logits, row stride ld)."""
+    """logp, and rel_lse for the backward, of each row's target token (rows of V logits,
+    row stride ld)."""
     _check(load_library().rmsnorm_token_logprob_fwd(_ptr(logits), ld, _ptr(targets),
-                                                    inv_temperature, _ptr(logp), _ptr(lse), M, V,
-                                                    _dt(x_dtype), _stream(stream)),
+                                                    inv_temperature, _ptr(logp), _ptr(rel_lse),
+                                                    M, V, _dt(x_dtype), _stream(stream)),
            "rmsnorm_token_logprob_fwd")
 
 
-def rmsnorm_token_logprob_bwd(logits, ld, targets, inv_temperature, lse, dlogp, scale, dlogits,
+def rmsnorm_token_logprob_bwd(logits, ld, targets, inv_temperature, rel_lse, dlogp, scale, dlogits,
                               ld_out, M, V, x_dtype, stream=None):
     """The logits' gradient from dlogp (times the device scalar `scale`, None for 1)."""
     _check(load_library().rmsnorm_token_logprob_bwd(_ptr(logits), ld, _ptr(targets),
-                                                    inv_temperature, _ptr(lse), _ptr(dlogp),
+                                                    inv_temperature, _ptr(rel_lse), _ptr(dlogp),
                                                     _ptr(scale), _ptr(dlogits), ld_out, M, V,
                                                     _dt(x_dtype), _stream(stream)),
            "rmsnorm_token_logprob_bwd")
 
 
 def rmsnorm_policy_loss_fwd(logits, ld, targets, inv_temperature, old_logp, ref_logp, advantages,
-                            weights, clip_low, clip_high, kl_coef, loss, token_loss, logp, lse,
+                            weights, clip_low, clip_high, kl_coef, loss, token_loss, logp, rel_lse,
                             dlogp, dlogits, ld_out, M, V, x_dtype, stream=None):
     """Clipped policy loss; dlogits (None to skip) takes its gradient in the same pass."""
     _check(load_library().rmsnorm_policy_loss_fwd(
         _ptr(logits), ld, _ptr(targets), inv_temperature, _ptr(old_logp), _ptr(ref_logp),
         _ptr(advantages), _ptr(weights), clip_low, clip_high, kl_coef, _ptr(loss),
-        _ptr(token_loss), _ptr(logp), _ptr(lse), _ptr(dlogp), _ptr(dlogits), ld_out, M, V,
+        _ptr(token_loss), _ptr(logp), _ptr(rel_lse), _ptr(dlogp), _ptr(dlogits), ld_out, M, V,
         _dt(x_dtype), _stream(stream)), "rmsnorm_policy_loss_fwd")
 
 
 def rmsnorm_preference_loss_fwd(logits, ld, targets, inv_temperature, ref_logp, cu_seqlens, pairs,
-                                beta, label_smoothing, loss, margins, logp, lse, dlogp, M, V,
+                                beta, label_smoothing, loss, margins, logp, rel_lse, dlogp, M, V,
                                 x_dtype, stream=None):
     """Preference loss over pairs of sequences (chosen first, then rejected)."""
     _check(load_library().rmsnorm_preference_loss_fwd(
         _ptr(logits), ld, _ptr(targets), inv_temperature, _ptr(ref_logp), _ptr(cu_seqlens), pairs,
-        beta, label_smoothing, _ptr(loss), _ptr(margins), _ptr(logp), _ptr(lse), _ptr(dlogp), M,
+        beta, label_smoothing, _ptr(loss), _ptr(margins), _ptr(logp), _ptr(rel_lse), _ptr(dlogp), M,
         V, _dt(x_dtype), _stream(stream)), "rmsnorm_preference_loss_fwd")
 
 

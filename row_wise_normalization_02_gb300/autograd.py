@@ -305,12 +305,12 @@ def _gradient_rows(rows):
     return flat[off:].as_strided((M, V), (ld, 1), off)
 
 
-def _logit_gradient(ctx, rows, targets, lse, dlogp, scale):
+def _logit_gradient(ctx, rows, targets, rel_lse, dlogp, scale):
     M, V = rows.shape
     dlogits = _gradient_rows(rows)
     with torch.cuda.device(rows.device):
-        rmsnorm_token_logprob_bwd(rows, _row_stride(rows), targets, ctx.inv_t, lse, dlogp, scale,
-                                  dlogits, _row_stride(dlogits), M, V, _dt(rows),
+        rmsnorm_token_logprob_bwd(rows, _row_stride(rows), targets, ctx.inv_t, rel_lse, dlogp,
+                                  scale, dlogits, _row_stride(dlogits), M, V, _dt(rows),
                                   _stream(rows.device))
     return dlogits
 
@@ -319,18 +319,18 @@ class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, targets, inv_t):
         M, V = rows.shape
-        logp, lse = torch.empty(2, M, dtype=torch.float32, device=rows.device)
+        logp, rel_lse = torch.empty(2, M, dtype=torch.float32, device=rows.device)
         with torch.cuda.device(rows.device):
-            rmsnorm_token_logprob_fwd(rows, _row_stride(rows), targets, inv_t, logp, lse, M, V,
+            rmsnorm_token_logprob_fwd(rows, _row_stride(rows), targets, inv_t, logp, rel_lse, M, V,
                                       _dt(rows), _stream(rows.device))
-        ctx.save_for_backward(rows, targets, lse)
+        ctx.save_for_backward(rows, targets, rel_lse)
         ctx.inv_t = inv_t
         return logp
 
     @staticmethod
     def backward(ctx, dlogp):
-        rows, targets, lse = ctx.saved_tensors
-        return _logit_gradient(ctx, rows, targets, lse, dlogp.contiguous(), None), None, None
+        rows, targets, rel_lse = ctx.saved_tensors
+        return _logit_gradient(ctx, rows, targets, rel_lse, dlogp.contiguous(), None), None, None
 
 
 class _PolicyLoss(torch.autograd.Function):
@@ -339,21 +339,22 @@ class _PolicyLoss(torch.autograd.Function):
                 kl_coef, inv_t):
         M, V = rows.shape
         loss = torch.empty((), dtype=torch.float32, device=rows.device)
-        token_loss, logp, lse, dlogp = torch.empty(4, M, dtype=torch.float32, device=rows.device)
+        token_loss, logp, rel_lse, dlogp = torch.empty(4, M, dtype=torch.float32,
+                                                       device=rows.device)
         with torch.cuda.device(rows.device):
             rmsnorm_policy_loss_fwd(rows, _row_stride(rows), targets, inv_t, old_logp, ref_logp,
                                     advantages, weights, clip_low, clip_high, kl_coef, loss,
-                                    token_loss, logp, lse, dlogp, None, 0, M, V, _dt(rows),
+                                    token_loss, logp, rel_lse, dlogp, None, 0, M, V, _dt(rows),
                                     _stream(rows.device))
-        ctx.save_for_backward(rows, targets, lse, dlogp)
+        ctx.save_for_backward(rows, targets, rel_lse, dlogp)
         ctx.inv_t = inv_t
         ctx.mark_non_differentiable(logp)
         return loss, logp
 
     @staticmethod
     def backward(ctx, dloss, _):
-        rows, targets, lse, dlogp = ctx.saved_tensors
-        return (_logit_gradient(ctx, rows, targets, lse, dlogp, dloss.contiguous()),
+        rows, targets, rel_lse, dlogp = ctx.saved_tensors
+        return (_logit_gradient(ctx, rows, targets, rel_lse, dlogp, dloss.contiguous()),
                 *(None,) * 9)
 
 
@@ -364,20 +365,20 @@ class _PreferenceLoss(torch.autograd.Function):
         pairs = (cu_seqlens.numel() - 1) // 2
         loss = torch.empty((), dtype=torch.float32, device=rows.device)
         margins = torch.empty(pairs, dtype=torch.float32, device=rows.device)
-        logp, lse, dlogp = torch.empty(3, M, dtype=torch.float32, device=rows.device)
+        logp, rel_lse, dlogp = torch.empty(3, M, dtype=torch.float32, device=rows.device)
         with torch.cuda.device(rows.device):
             rmsnorm_preference_loss_fwd(rows, _row_stride(rows), targets, inv_t, ref_logp,
                                         cu_seqlens, pairs, beta, label_smoothing, loss, margins,
-                                        logp, lse, dlogp, M, V, _dt(rows), _stream(rows.device))
-        ctx.save_for_backward(rows, targets, lse, dlogp)
+                                        logp, rel_lse, dlogp, M, V, _dt(rows), _stream(rows.device))
+        ctx.save_for_backward(rows, targets, rel_lse, dlogp)
         ctx.inv_t = inv_t
         ctx.mark_non_differentiable(margins)
         return loss, margins
 
     @staticmethod
     def backward(ctx, dloss, _):
-        rows, targets, lse, dlogp = ctx.saved_tensors
-        return (_logit_gradient(ctx, rows, targets, lse, dlogp, dloss.contiguous()),
+        rows, targets, rel_lse, dlogp = ctx.saved_tensors
+        return (_logit_gradient(ctx, rows, targets, rel_lse, dlogp, dloss.contiguous()),
                 *(None,) * 6)
 
 

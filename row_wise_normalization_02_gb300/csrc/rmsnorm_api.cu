@@ -1918,6 +1918,7 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
 // ---------------------------------------------------------------- token losses
 
 constexpr int64_t kLossMaxM = (int64_t(1) << 28) - 1;
+constexpr int64_t kLossOneCta = 32768;
 
 // Operands of a loss call, checked for NULL, alignment and overlap as they are
 // listed.
@@ -1966,8 +1967,8 @@ size_t rows_span(int64_t M, int64_t V, int64_t ld, int es, rmsnorm_status_t* st)
 }
 
 rmsnorm_status_t check_loss(int64_t M, int64_t V, double inv_t, int xd) {
-  if (M < 0 || M > kLossMaxM || V < 1 || V > kMaxN || !(inv_t > 0.0) || !isfinite(inv_t) ||
-      !isfinite((float)inv_t * 1.5f) || !((float)inv_t > 0.f))
+  // (the bounds keep both parts of log2(e) / temperature normal numbers)
+  if (M < 0 || M > kLossMaxM || V < 1 || V > kMaxN || !(inv_t >= 1e-9) || !(inv_t <= 1e9))
     return RMSNORM_ERR_INVALID_ARG;
   if (xd != kF32 && xd != kBF16) return RMSNORM_ERR_UNSUPPORTED_DTYPE;
   return RMSNORM_OK;
@@ -1981,9 +1982,12 @@ LossParams loss_params(const void* logits, int64_t ld, const int64_t* targets, d
   p.targets = targets;
   p.M = M;
   p.V = (int)V;
-  p.inv_t = inv_t;
   p.inv_tf = (float)inv_t;
-  p.c1 = (float)(inv_t * 1.4426950408889634);
+  p.inv_tlo = (float)(inv_t - (double)p.inv_tf);
+  const double c = inv_t * 1.4426950408889634;   // log2(e)
+  p.c_hi = (float)c;
+  if ((double)p.c_hi >= c) p.c_hi = nextafterf(p.c_hi, 0.f);
+  p.c_lo = (float)(c - (double)p.c_hi);
   return p;
 }
 
@@ -2000,22 +2004,71 @@ void add_logits(LossOperands* ops, const void* logits, int64_t ld, void* dlogits
   if (!in_place) ops->add(dlogits, out, (size_t)es, true);
 }
 
-// The row kernel: a CTA per row, or clusters of up to eight per row while the
-// SMs would not have two CTAs each and a CTA keeps a batch of vectors.
-rmsnorm_status_t launch_loss_rows(int mode, int xd, const LossParams& p, cudaStream_t stream) {
+// The kernel over the rows.
+rmsnorm_status_t launch_loss_rows(int mode, int xd, LossParams p, cudaStream_t stream) {
   int dev;
   rmsnorm_status_t st = current_device(&dev);
   if (st != RMSNORM_OK) return st;
   DevInfo di;
   cudaError_t e = device_info(dev, &di);
   if (e != cudaSuccess) return cuda_fail(e, "device attributes");
+  p.wait_limit = wait_limit();
+  p.status = di.status;
   const int64_t nvec = p.V / per_vec(xd);
-  int cl = 1;
-  while (cl < 8 && p.M * cl * 2 <= 2 * di.sms && nvec / (2 * cl) >= kLossThreads) cl *= 2;
-  int threads = (int)((nvec / cl + kLossBatch - 1) / kLossBatch);
-  threads = threads >= kLossThreads ? kLossThreads : round_up(threads < 64 ? 64 : threads, 32);
-  const LossKernel fn = xd == kF32 ? get_loss_row_f32(mode, cl) : get_loss_row_bf16(mode, cl);
-  e = launch_in_clusters(cl > 1 ? cl : 0, fn, (int)(p.M * cl), threads, 0, stream, p);
+  const Force& force = read_force();
+  int cl = 1, threads, smem = 0;
+  int64_t grid = 0;
+  const int64_t slots = (int64_t)di.sms * 1024;   // threads at 64 registers each
+  if (mode != kLossPolicyGrad) {
+    // A CTA per row, small enough that a thread has some 64 vectors and CTAs at
+    // other points of their rows fill the SM (fwd, bf16: 4096 x 131072 128 threads
+    // 128 us, 256 131, 64 144; 8192 x 32768 64 threads 68, 256 74; 16384 x 8192 32
+    // threads 38, 128 43).  Few rows: larger CTAs, then clusters of up to eight per
+    // row, until the SMs are full (600 x 32003 fp32: 256 threads 12.5, 128 15.8; 64 x
+    // 131072 bf16: eight CTAs of 256 a row 11, one 14).
+    threads = 128;
+    while (threads > 32 && nvec < 64 * threads) threads /= 2;
+    while (threads < kLossThreads && p.M * threads * 2 <= slots && nvec >= 8 * threads)
+      threads *= 2;
+    while (cl < 8 && p.M * cl * threads * 2 <= slots && nvec >= 2 * cl * kLossBatch * threads)
+      cl *= 2;
+    if (force.on && force.cl) cl = force.cl;
+    if (force.on && force.threads) threads = force.threads;
+    if (threads < 32 || threads > kLossThreads || threads % 32) return RMSNORM_ERR_INVALID_ARG;
+    grid = p.M * cl;
+  } else {
+    // CTAs that hold three quarters or more of their part of a row in their ring
+    // (12 of 16 vectors a thread): one CTA of up to 256 threads, or a cluster of
+    // CTAs of 128 (4096 x 131072 bf16: eight of 128 threads 363 us, four of 256 376,
+    // two of 512 377; 8192 x 32768: one of 256 184, two of 128 196).  Few rows: more
+    // CTAs a row.
+    threads = 32;
+    while (threads < 256 && nvec > 16 * threads) threads *= 2;
+    if (nvec > 16 * 256 && nvec <= 8 * 16 * 128) threads = 128;
+    while (cl < 8 && threads >= 128 &&
+           (nvec > 16 * threads * cl || (p.M * cl * threads * 2 <= slots &&
+                                         nvec >= 2 * cl * kLossBatch * threads)))
+      cl *= 2;
+    if (force.on && force.cl) cl = force.cl;
+    if (force.on && force.threads) threads = force.threads;
+    smem = kLossStages * kLossBatch * 16 * threads;
+  }
+  const LossKernel fn =
+      xd == kF32 ? get_loss_rows_f32(mode, cl, threads) : get_loss_rows_bf16(mode, cl, threads);
+  if (!fn) return RMSNORM_ERR_INVALID_ARG;
+  if (grid == 0) {   // persistent: the clusters that the device holds at once
+    const void* f = reinterpret_cast<const void*>(fn);
+    int held = 0;
+    // (the kernel's static shared memory counts against the same default limit)
+    if ((e = ensure_smem(f, dev, smem + 1024)) != cudaSuccess ||
+        (e = occupancy(f, dev, threads, smem, &held, cl > 1 ? cl : 0)) != cudaSuccess) {
+      cudaGetLastError();
+      return cuda_fail(e, "occupancy of the policy loss kernel");
+    }
+    const int64_t cap = cl > 1 ? held : (int64_t)held * di.sms;
+    grid = (p.M < cap ? p.M : cap) * cl;
+  }
+  e = launch_in_clusters(cl > 1 ? cl : 0, fn, (int)grid, threads, smem, stream, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return cuda_fail(e, "token log-probability launch");
@@ -2034,7 +2087,7 @@ rmsnorm_status_t launch_loss(LossKernel fn, int64_t grid, int threads, const Los
 }
 
 rmsnorm_status_t token_logprob_fwd_impl(const void* logits, int64_t ld, const int64_t* targets,
-                                        double inv_t, float* logp, float* lse, int64_t M,
+                                        double inv_t, float* logp, float* rel_lse, int64_t M,
                                         int64_t V, int xd, cudaStream_t stream) {
   rmsnorm_status_t st = check_loss(M, V, inv_t, xd);
   if (st != RMSNORM_OK) return st;
@@ -2044,16 +2097,16 @@ rmsnorm_status_t token_logprob_fwd_impl(const void* logits, int64_t ld, const in
   const size_t rows = (size_t)M * 4;
   ops.add(targets, rows * 2, 8, false);
   ops.add(logp, rows, 4, true);
-  ops.add(lse, rows, 4, true);
+  ops.add(rel_lse, rows, 4, true);
   if ((st = ops.check()) != RMSNORM_OK) return st;
   LossParams p = loss_params(logits, ld, targets, inv_t, M, V);
   p.logp = logp;
-  p.lse = lse;
+  p.lse = rel_lse;
   return launch_loss_rows(kLossLogprob, xd, p, stream);
 }
 
 rmsnorm_status_t token_logprob_bwd_impl(const void* logits, int64_t ld, const int64_t* targets,
-                                        double inv_t, const float* lse, const float* dlogp,
+                                        double inv_t, const float* rel_lse, const float* dlogp,
                                         const float* scale, void* dlogits, int64_t ld_out,
                                         int64_t M, int64_t V, int xd, cudaStream_t stream) {
   rmsnorm_status_t st = check_loss(M, V, inv_t, xd);
@@ -2063,17 +2116,18 @@ rmsnorm_status_t token_logprob_bwd_impl(const void* logits, int64_t ld, const in
   add_logits(&ops, logits, ld, dlogits, ld_out, M, V, xd, true);
   const size_t rows = (size_t)M * 4;
   ops.add(targets, rows * 2, 8, false);
-  ops.add(lse, rows, 4, false);
+  ops.add(rel_lse, rows, 4, false);
   ops.add(dlogp, rows, 4, false);
   ops.add(scale, 4, 4, false, true);
   if ((st = ops.check()) != RMSNORM_OK) return st;
   LossParams p = loss_params(logits, ld, targets, inv_t, M, V);
-  p.lse = const_cast<float*>(lse);
+  p.lse = const_cast<float*>(rel_lse);
   p.dlogp_in = dlogp;
   p.scale = scale;
   p.dlogits = dlogits;
   p.ld_out = ld_out;
-  const int64_t per = (int64_t)kLossBwdVecs * per_vec(xd);
+  p.whole_rows = dlogits == logits;
+  const int64_t per = p.whole_rows ? V : (int64_t)kLossBwdVecs * per_vec(xd);
   const int64_t items = M * ((V + per - 1) / per), cap = int64_t(1) << 30;
   return launch_loss(xd == kF32 ? get_loss_bwd_f32() : get_loss_bwd_bf16(),
                      items < cap ? items : cap, kLossThreads, p, stream,
@@ -2084,7 +2138,7 @@ rmsnorm_status_t policy_loss_impl(const void* logits, int64_t ld, const int64_t*
                                   double inv_t, const float* old_logp, const float* ref_logp,
                                   const float* advantages, const float* weights, float clip_low,
                                   float clip_high, float kl_coef, float* loss, float* token_loss,
-                                  float* logp, float* lse, float* dlogp, void* dlogits,
+                                  float* logp, float* rel_lse, float* dlogp, void* dlogits,
                                   int64_t ld_out, int64_t M, int64_t V, int xd,
                                   cudaStream_t stream) {
   rmsnorm_status_t st = check_loss(M, V, inv_t, xd);
@@ -2101,11 +2155,11 @@ rmsnorm_status_t policy_loss_impl(const void* logits, int64_t ld, const int64_t*
   ops.add(advantages, rows, 4, false);
   ops.add(weights, rows, 4, false, true);
   ops.add(loss, 4, 4, true);
-  for (float* out : {token_loss, logp, lse, dlogp}) ops.add(out, rows, 4, true);
+  for (float* out : {token_loss, logp, rel_lse, dlogp}) ops.add(out, rows, 4, true);
   if ((st = ops.check()) != RMSNORM_OK) return st;
   LossParams p = loss_params(logits, ld, targets, inv_t, M, V);
   p.logp = logp;
-  p.lse = lse;
+  p.lse = rel_lse;
   p.dlogp = dlogp;
   p.old_logp = old_logp;
   p.ref_logp = ref_logp;
@@ -2128,7 +2182,7 @@ rmsnorm_status_t policy_loss_impl(const void* logits, int64_t ld, const int64_t*
 rmsnorm_status_t preference_loss_impl(const void* logits, int64_t ld, const int64_t* targets,
                                       double inv_t, const float* ref_logp, const int64_t* cu,
                                       int64_t pairs, float beta, float smoothing, float* loss,
-                                      float* margins, float* logp, float* lse, float* dlogp,
+                                      float* margins, float* logp, float* rel_lse, float* dlogp,
                                       int64_t M, int64_t V, int xd, cudaStream_t stream) {
   rmsnorm_status_t st = check_loss(M, V, inv_t, xd);
   if (st != RMSNORM_OK) return st;
@@ -2143,11 +2197,11 @@ rmsnorm_status_t preference_loss_impl(const void* logits, int64_t ld, const int6
   ops.add(cu, (size_t)(2 * pairs + 1) * 8, 8, false);
   ops.add(loss, 4, 4, true);
   ops.add(margins, (size_t)pairs * 4, 4, true);
-  for (float* out : {logp, lse, dlogp}) ops.add(out, rows, 4, true);
+  for (float* out : {logp, rel_lse, dlogp}) ops.add(out, rows, 4, true);
   if ((st = ops.check()) != RMSNORM_OK) return st;
   LossParams p = loss_params(logits, ld, targets, inv_t, M, V);
   p.logp = logp;
-  p.lse = lse;
+  p.lse = rel_lse;
   p.dlogp = dlogp;
   p.ref_logp = ref_logp;
   p.cu = cu;
@@ -2157,8 +2211,13 @@ rmsnorm_status_t preference_loss_impl(const void* logits, int64_t ld, const int6
   p.margins = margins;
   p.loss = loss;
   if (M > 0 && (st = launch_loss_rows(kLossPreference, xd, p, stream)) != RMSNORM_OK) return st;
-  if ((st = launch_loss(get_loss_pairs(), pairs, kLossThreads, p, stream,
-                        "preference margins launch")) != RMSNORM_OK)
+  // one CTA for all of it up to kLossOneCta rows (8192 rows: 4 us against 3 + 2 in two
+  // launches), else a CTA per pair and one for the mean
+  const bool one = M <= kLossOneCta;
+  if ((st = launch_loss(one ? get_loss_pairs_all() : get_loss_pairs(), one ? 1 : pairs,
+                        one ? 1024 : kLossThreads, p, stream, "preference margins launch")) !=
+          RMSNORM_OK ||
+      one)
     return st;
   return launch_loss(get_loss_pairs_mean(), 1, kLossThreads, p, stream, "preference loss launch");
 }
@@ -2526,20 +2585,20 @@ rmsnorm_status_t rmsnorm_rope_bwd(const rmsnorm_heads_t* dq_out, const rmsnorm_h
 
 rmsnorm_status_t rmsnorm_token_logprob_fwd(const void* logits, int64_t ld,
                                            const int64_t* targets, double inv_temperature,
-                                           float* logp, float* lse, int64_t M, int64_t V,
+                                           float* logp, float* rel_lse, int64_t M, int64_t V,
                                            rmsnorm_dtype_t x_dtype, cudaStream_t stream) {
-  return token_logprob_fwd_impl(logits, ld, targets, inv_temperature, logp, lse, M, V,
+  return token_logprob_fwd_impl(logits, ld, targets, inv_temperature, logp, rel_lse, M, V,
                                 (int)x_dtype, stream);
 }
 
 rmsnorm_status_t rmsnorm_token_logprob_bwd(const void* logits, int64_t ld,
                                            const int64_t* targets, double inv_temperature,
-                                           const float* lse, const float* dlogp,
+                                           const float* rel_lse, const float* dlogp,
                                            const float* scale, void* dlogits, int64_t ld_out,
                                            int64_t M, int64_t V, rmsnorm_dtype_t x_dtype,
                                            cudaStream_t stream) {
-  return token_logprob_bwd_impl(logits, ld, targets, inv_temperature, lse, dlogp, scale, dlogits,
-                                ld_out, M, V, (int)x_dtype, stream);
+  return token_logprob_bwd_impl(logits, ld, targets, inv_temperature, rel_lse, dlogp, scale,
+                                dlogits, ld_out, M, V, (int)x_dtype, stream);
 }
 
 rmsnorm_status_t rmsnorm_policy_loss_fwd(const void* logits, int64_t ld, const int64_t* targets,
@@ -2547,11 +2606,11 @@ rmsnorm_status_t rmsnorm_policy_loss_fwd(const void* logits, int64_t ld, const i
                                          const float* ref_logp, const float* advantages,
                                          const float* weights, float clip_low, float clip_high,
                                          float kl_coef, float* loss, float* token_loss,
-                                         float* logp, float* lse, float* dlogp, void* dlogits,
+                                         float* logp, float* rel_lse, float* dlogp, void* dlogits,
                                          int64_t ld_out, int64_t M, int64_t V,
                                          rmsnorm_dtype_t x_dtype, cudaStream_t stream) {
   return policy_loss_impl(logits, ld, targets, inv_temperature, old_logp, ref_logp, advantages,
-                          weights, clip_low, clip_high, kl_coef, loss, token_loss, logp, lse,
+                          weights, clip_low, clip_high, kl_coef, loss, token_loss, logp, rel_lse,
                           dlogp, dlogits, ld_out, M, V, (int)x_dtype, stream);
 }
 
@@ -2559,11 +2618,11 @@ rmsnorm_status_t rmsnorm_preference_loss_fwd(const void* logits, int64_t ld,
                                              const int64_t* targets, double inv_temperature,
                                              const float* ref_logp, const int64_t* cu_seqlens,
                                              int64_t pairs, float beta, float label_smoothing,
-                                             float* loss, float* margins, float* logp, float* lse,
+                                             float* loss, float* margins, float* logp, float* rel_lse,
                                              float* dlogp, int64_t M, int64_t V,
                                              rmsnorm_dtype_t x_dtype, cudaStream_t stream) {
   return preference_loss_impl(logits, ld, targets, inv_temperature, ref_logp, cu_seqlens, pairs,
-                              beta, label_smoothing, loss, margins, logp, lse, dlogp, M, V,
+                              beta, label_smoothing, loss, margins, logp, rel_lse, dlogp, M, V,
                               (int)x_dtype, stream);
 }
 

@@ -275,10 +275,10 @@ struct LossParams {
   const int64_t* targets;    // negative: the row takes no part
   int64_t M;
   int V;
-  double inv_t;              // 1 / temperature
-  float inv_tf, c1;          // the same in fp32, and times log2(e)
+  float inv_tf, inv_tlo;     // 1 / temperature in two parts
+  float c_hi, c_lo;          // times log2(e), in two parts: c_hi rounded down, c_lo > 0
   float* logp;
-  float* lse;
+  float* lse;                // the row's log-sum-exp seen from its target: -logp
   float* dlogp;              // policy, preference: d loss / d logp of each row
   // policy
   const float* old_logp;
@@ -296,21 +296,27 @@ struct LossParams {
   // gradient: the backward, and the policy loss in one pass with it
   const float* scale;        // backward: device scalar that multiplies dlogp, or null
   const float* dlogp_in;     // backward
+  bool whole_rows;           // backward: a CTA takes whole rows (dlogits is logits)
   void* dlogits;
   int64_t ld_out;
+  long long wait_limit;      // clock cycles before a wait for a cluster's peers gives up
+  unsigned* status;          // device status word (kStatus* bits)
 };
 enum LossMode : int { kLossLogprob = 0, kLossPolicy = 1, kLossPolicyGrad = 2, kLossPreference = 3 };
 using LossKernel = void (*)(LossParams);
-// Row kernel of a mode for clusters of `cluster` CTAs per row.
-LossKernel get_loss_row_f32(int mode, int cluster);
-LossKernel get_loss_row_bf16(int mode, int cluster);
+// Kernel of a mode for clusters of `cluster` CTAs per row (with the gradient: for
+// CTAs of `threads` threads).
+LossKernel get_loss_rows_f32(int mode, int cluster, int threads);
+LossKernel get_loss_rows_bf16(int mode, int cluster, int threads);
 LossKernel get_loss_bwd_f32();
 LossKernel get_loss_bwd_bf16();
 LossKernel get_loss_sum();        // loss = sum of token_loss, one CTA
 LossKernel get_loss_pairs();      // one CTA per pair: margins, dlogp
+LossKernel get_loss_pairs_all();  // one CTA: margins, dlogp and loss
 LossKernel get_loss_pairs_mean(); // loss = mean over the pairs, one CTA
 constexpr int kLossThreads = 256;
-constexpr int kLossBatch = 4;     // 16-byte vectors a thread has in flight
+constexpr int kLossBatch = 4;     // 16-byte vectors a thread takes at a time
+constexpr int kLossStages = 3;    // batches in a thread's ring (loss with gradient)
 constexpr int kLossBwdVecs = kLossThreads * kLossBatch;   // vectors of a row per backward CTA
 
 // Threads per CTA of the subwarp families; upper bound of the per-row CTAs.

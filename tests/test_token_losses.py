@@ -10,10 +10,13 @@ temperature, the exponents of a row's terms:
     roundings: a thread's share over its four accumulators, V / 4 / 64 at the fewest
     threads and V / 4 / 256 for long rows, and 40 for the batches' rescaling, the
     shuffles, the warps and the cluster.
-  * lse and logp: that, absolutely (d log s = ds / s), and one rounding u of the result.
-  * p_j = exp(z_j - lse): the error of lse and the roundings of z_j - lse and of lse
-    itself, u (2 |z_j| + 2 |lse|) + 2^-21, relative.  dlogits = g ([j = t] - p): that
-    times p |g|, and three roundings of the result.
+  * logp, and rel_lse = -logp: that, absolutely (d log s = ds / s), and one rounding u of
+    the result.
+  * p_j = exp(z_j - z_t - rel): the error of rel and the roundings of z_j - z_t, of its
+    product with the two parts of the scale and of rel, u (4 |z_j - z_t| + 4 |rel|) +
+    2^-21, relative (where rel > 64 the sum is taken again, and the exponents are those
+    from the maximum: smaller).  dlogits = g ([j = t] - p): that times p |g|, and three
+    roundings of the result.
   * the policy's ratio carries the error of logp; loss terms and slopes a few roundings
     more (POINT = 2^-20) of the magnitudes of their parts.
   * margins: the errors of their rows' logp added up, times beta, and a rounding.
@@ -66,21 +69,23 @@ class Ref:
         self.live = t >= 0
         self.t = t.clamp(min=0)
         m = self.z.amax(1, keepdim=True)
-        self.lse = (m[:, 0] + (self.z - m).exp().sum(1).log())
-        self.logp = self.z.gather(1, self.t[:, None])[:, 0] - self.lse
+        log_s = (self.z - m).exp().sum(1).log()
+        self.p = (self.z - m - log_s[:, None]).exp()
+        # the difference first: 64 bits too lose log s beside a mask's lowest value
+        self.zt = self.z.gather(1, self.t[:, None])
+        self.logp = (self.z.gather(1, self.t[:, None]) - m)[:, 0] - log_s
         self.logp[~self.live] = 0
-        self.lse[~self.live] = 0
+        self.rel = -self.logp
         self.inv_t = inv_t
 
     def grad(self, dlogp):
         """Gradient for dlogp, and its tolerance for an error `rel` of g."""
         g = torch.where(self.live, dlogp, 0.0)[:, None] * self.inv_t
-        p = (self.z - self.lse[:, None]).exp()
-        p[~self.live] = 0
+        p = torch.where(self.live[:, None], self.p, 0.0)
         one = torch.zeros_like(p).scatter_(1, self.t[:, None], 1.0)
         V = p.shape[1]
-        size = torch.where(self.z.isinf(), 0.0, self.z.abs())    # p is 0 there
-        err = p * (logp_tol(V) + U * (2 * size + 2 * self.lse.abs()[:, None]) + 2.0 ** -21)
+        size = torch.where(self.z.isinf(), 0.0, (self.z - self.zt).abs())    # p is 0 there
+        err = p * (logp_tol(V) + U * (4 * size + 4 * self.rel.abs()[:, None]) + 2.0 ** -21)
         return g * (one - p), g.abs() * (err + 3 * U * (one + p))
 
 
@@ -121,7 +126,7 @@ def check_logprob(x, t, dt, inv_t=1.0, out=None):
     r = Ref(x, t, inv_t)
     logp, lse = fwd(x, t, inv_t, dt)
     close(logp, r.logp, logp_tol(V) + U * r.logp.abs(), "logp")
-    close(lse, r.lse, logp_tol(V) + U * r.lse.abs(), "lse")
+    assert torch.equal(lse, -logp)
     dlogp = torch.randn(M, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
     scale = torch.tensor(1.5, device="cuda")
     d = bwd(x, t, lse, dlogp, scale, inv_t, dt, out)
@@ -176,16 +181,16 @@ def test_large_magnitudes_and_order(dt):
         logp, lse = fwd(x, t, 1.0, dt)
         # logp is the difference of values far larger than the softmax's spread
         close(logp, r.logp, logp_tol(30000) + U * r.logp.abs(), "logp")
-        close(lse, r.lse, logp_tol(30000) + U * r.lse.abs(), "lse")
-        # an lse too large for its fp32 digits: the backward takes the sum again, and a term is
-        # off by its exponent's rounding, 2 u |z - max|; smaller ones are within the usual bound
+        assert torch.equal(lse, -logp)
+        # a rel_lse too large for its fp32 digits: the backward takes the sum again, and a term
+        # is off by its exponent's rounding, 2 u |z - max|; smaller ones are within the usual bound
         dlogp = torch.linspace(-1, 1, 8, device="cuda")
-        far = r.lse.abs() > 2048
-        p = torch.where(r.live[:, None], (r.z - r.lse[:, None]).exp(), 0.0)
+        far = r.rel > 64
+        p = torch.where(r.live[:, None], r.p, 0.0)
         one = torch.zeros_like(p).scatter_(1, r.t[:, None], 1.0)
         want = torch.where(r.live, dlogp.double(), 0.0)[:, None] * (one - p)
-        size = torch.where(far[:, None], 2 * (r.z - r.z.amax(1, keepdim=True)).abs(),
-                           2 * r.z.abs() + 2 * r.lse.abs()[:, None])
+        size = torch.where(far[:, None], 4 * (r.z - r.z.amax(1, keepdim=True)).abs(),
+                           4 * (r.z - r.zt).abs() + 4 * r.rel.abs()[:, None])
         tol = dlogp.abs()[:, None] * (p * (logp_tol(30000) + U * size + 2.0 ** -21) +
                                       3 * U * (one + p)) + half_step(dt) * want.abs() * (dt == "bf16")
         close(bwd(x, t, lse, dlogp, dt=dt), want, tol, "dlogits")
@@ -225,8 +230,9 @@ def test_masked_vocabulary_and_special_rows(dt):
     assert logp[3] == float("-inf") and bool(d[3].isfinite().all())
     for bad in (1, 4, 5, 7, 8):
         assert bool(logp[bad].isnan()) and bool(d[bad].isnan().any()), bad
-    assert bool(lse[7].isfinite()) and bool(d[7].isnan().all())
+    assert bool(d[7].isnan().all())
     assert logp[11] == 0 and lse[11] == 0 and not d[11].any()
+    assert torch.equal(bwd(x, t, lse, dlogp, dt=dt, out=x).isnan(), d.isnan())    # in place
 
 
 # ---------------------------------------------------------------- policy loss
@@ -284,17 +290,18 @@ def test_policy_loss(M, V, pad, inv_t, kl, dt):
     old, ref, A, w = policy_inputs(r, M, kl is not None)
     for weights in (w, None):
         term, slope, tol = policy_ref(r, old, ref, A, weights, kl or 0.0)
-        loss, token, logp, lse, dlogp, d = policy(x, t, old, ref, A, weights, kl or 0.0, dt, inv_t)
-        close(logp, r.logp, logp_tol(V) + U * r.logp.abs(), "logp")
-        close(token, term, tol, "token loss")
-        close(loss, term.sum(), tol.sum() + U * term.sum().abs(), "loss")
-        close(dlogp, slope, tol, "dlogp")
-        check_grad(d, r, slope, dt, "dlogits", tol)
-        # without the gradient, and the gradient from the backward
-        l2, tk2, lp2, ls2, dl2, _ = policy(x, t, old, ref, A, weights, kl or 0.0, dt, inv_t,
-                                           want=False)
-        for a, b in ((loss, l2), (token, tk2), (logp, lp2), (lse, ls2), (dlogp, dl2)):
-            assert torch.equal(a, b)
+        # with the gradient in the same pass, and without it (another kernel)
+        for want in (True, False):
+            loss, token, logp, lse, dlogp, d = policy(x, t, old, ref, A, weights, kl or 0.0, dt,
+                                                      inv_t, want=want)
+            close(logp, r.logp, logp_tol(V) + U * r.logp.abs(), "logp")
+            assert torch.equal(lse, -logp)
+            close(token, term, tol, "token loss")
+            close(loss, term.sum(), tol.sum() + U * term.sum().abs(), "loss")
+            close(dlogp, slope, tol, "dlogp")
+            if want:
+                check_grad(d, r, slope, dt, "dlogits", tol)
+                one_pass = d
         check_grad(bwd(x, t, lse, dlogp, None, inv_t, dt), r, slope, dt, "backward", tol)
     # in place, and rows that start elsewhere modulo 16 bytes
     other = torch.empty(M * (V + 3) + 16, dtype=TD[dt], device="cuda")[1:1 + M * (V + 3)]
@@ -303,7 +310,7 @@ def test_policy_loss(M, V, pad, inv_t, kl, dt):
     check_grad(other, r, slope, dt, "dlogits elsewhere", tol)
     x2 = x.clone() if pad == 0 else x
     policy(x2, t, old, ref, A, None, kl or 0.0, dt, inv_t, out=x2)
-    assert torch.equal(x2, d)
+    assert torch.equal(x2, one_pass)
 
 
 @gpu
@@ -395,7 +402,8 @@ def preference_ref(r, ref, cu, beta, ls):
 @pytest.mark.parametrize("cu,M,V", [
     ([0, 1, 2], 2, 30), ([0, 0, 5], 5, 100), ([0, 5, 5], 5, 100), ([0, 0, 0], 3, 100),
     ([2, 30, 41, 41, 80], 90, 1001), ([0, 300, 301, 500, 777, 900, 1200], 1203, 500),
-    ([3, 10, 20], 30, 60000)])
+    ([3, 10, 20], 30, 60000), (list(range(0, 82, 1)) + [90, 100, 300], 310, 70),
+    ([0, 20000, 20001, 39000, 40000], 40000, 50)])
 def test_preference_loss(cu, M, V, with_ref, dt):
     x, t, _ = rows(M, V, dt, seed=V)
     r = Ref(x, t, 1.0)
