@@ -361,9 +361,10 @@ typedef struct rmsnorm_rope {
  * side out of one buffer are apart: q and k of a fused projection's rows (equal
  * token strides), or heads in turn (equal head strides that divide the token
  * strides).  D <= RMSNORM_ROPE_MAX_D,
- * T < 2^30, Hq + Hk <= 2^16.  Rows whose starts, strides and halves fall on
- * 16-byte vectors (D and R multiples of two vectors, 32 bytes), of at most
- * 64 vectors, take the vectorised kernels; any other layout a scalar one.
+ * T < 2^30, Hq + Hk <= 2^16.  The kernels work in vectors of 16 bytes where
+ * starts and strides are multiples of that and D and R of two of them, of 8, 4
+ * or 2 bytes otherwise; rows beyond 64 vectors of 16 bytes or 256 smaller ones
+ * take a scalar kernel.
  */
 rmsnorm_status_t rmsnorm_rope_fwd(const rmsnorm_heads_t* q, const rmsnorm_heads_t* k,
                                   const void* q_gamma, const void* k_gamma,

@@ -1687,17 +1687,34 @@ bool spans_overlap(const Span& a, const Span& b, int64_t D, int es) {
   return true;
 }
 
-bool view_vec_ok(const rmsnorm_heads_t& v, int es) {
-  return aligned_to(v.data, 16) && v.stride_token * es % 16 == 0 && v.stride_head * es % 16 == 0;
+// Largest power of two, at most 16, that a view's start and strides are multiples
+// of, in bytes.
+int view_alignment(const rmsnorm_heads_t& v, int64_t T, int es) {
+  uint64_t bits = (uint64_t)reinterpret_cast<uintptr_t>(v.data) | 16;
+  if (T > 1) bits |= (uint64_t)(v.stride_token * es);
+  if (v.heads > 1) bits |= (uint64_t)(v.stride_head * es);
+  return (int)(bits & (~bits + 1));
 }
 
-// Lanes per row for D elements as two vectors per lane, or 0 (scalar kernel).
-int rope_lanes(int64_t D, int64_t R, int xd, bool views_ok) {
-  const int64_t pair = 2 * per_vec(xd);
-  if (!views_ok || D % pair || R % pair || D > 32 * pair) return 0;
-  int g = 4;
-  while (g * pair < D) g *= 2;
-  return g;
+// Shape of the vectorised kernels for operands aligned to `align` bytes: the
+// largest vectors that rows and halves divide into, G lanes of L units (two
+// vectors) per row.  All zero: the scalar kernel (rows beyond 64 such vectors of
+// 16 bytes or 256 smaller ones).
+void rope_shape(int64_t D, int64_t R, int xd, int align, int* e_out, int* g_out, int* l_out) {
+  *e_out = *g_out = *l_out = 0;
+  const int full = per_vec(xd);
+  for (int e = align / esize(xd); e > 0; e /= 2) {
+    if (D % (2 * e) || R % (2 * e)) continue;
+    const int64_t units = D / (2 * e);
+    int g = e == full ? 4 : 16, l = 1;
+    while (g < 32 && g < units) g *= 2;
+    while (e < full && l < 4 && (int64_t)g * l < units) l *= 2;
+    if ((int64_t)g * l < units) return;
+    *e_out = e;
+    *g_out = g;
+    *l_out = l;
+    return;
+  }
 }
 
 // Work items: a token's rows in chunks, so many that small batches spread over
@@ -1759,7 +1776,7 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
   const int es = esize(xd);
   Span spans[16];
   int ns = 0;   // at most 3 views, gamma and dgamma per side, 2 of the rotation, the workspace
-  bool views_ok = true;
+  int align = 16;
   for (int i = 0; i < 2; ++i) {
     if (heads[i] == 0) continue;
     const rmsnorm_heads_t* views[3] = {!bwd || norm ? x[i] : nullptr, bwd ? dy[i] : nullptr,
@@ -1773,7 +1790,8 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
         return RMSNORM_ERR_INVALID_ARG;
       if (T > 0 && !v->data) return RMSNORM_ERR_INVALID_ARG;
       if (T > 0 && !aligned_to(v->data, (size_t)es)) return RMSNORM_ERR_MISALIGNED;
-      views_ok = views_ok && view_vec_ok(*v, es);
+      const int va = view_alignment(*v, T, es);
+      align = va < align ? va : align;
       // in place: the output over the view it replaces, with its strides
       const rmsnorm_heads_t* from = bwd ? dy[i] : x[i];
       const bool in_place = j == 2 && v->data == from->data &&
@@ -1786,7 +1804,7 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
       if (!aligned_to(gamma[i], (size_t)esize(wd)) ||
           (dgamma[i] && !aligned_to(dgamma[i], 4)))
         return RMSNORM_ERR_MISALIGNED;
-      views_ok = views_ok && aligned_to(gamma[i], 16);
+      if (align == 16 && !aligned_to(gamma[i], 16)) align = 8;   // 16-byte vectors of it too
       spans[ns++] = Span{gamma[i], (size_t)D * esize(wd), false, nullptr};
       if (dgamma[i]) spans[ns++] = Span{dgamma[i], (size_t)D * 4, true, nullptr};
     }
@@ -1828,8 +1846,10 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
 
   const int64_t R = rope->rotary_dim;
   const bool norm_bwd = bwd && norm;
-  const int g = rope_lanes(D, R, xd, views_ok);
-  const RopeKernel fn = rope_kernel(RopeKey{xd, wd, norm_bwd, norm, rope->pairs == 1, g});
+  int e_vec, g, l;
+  rope_shape(D, R, xd, align, &e_vec, &g, &l);
+  const RopeKernel fn =
+      rope_kernel(RopeKey{xd, wd, norm_bwd, norm, rope->pairs == 1, e_vec, g, l});
   if (!fn) return RMSNORM_ERR_INVALID_ARG;
 
   RopeParams p = {};
@@ -1870,7 +1890,9 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
   int threads = kRopeThreads, smem;
   if (g > 0) {
     const int step = 32 / g, warps = kRopeThreads / 32;
-    smem = warps * angles + (norm_bwd ? warps * (int)D * 4 : 0);
+    const int step_bytes = 2 * l * e_vec * es * kRopeThreads;   // of one operand
+    smem = warps * angles + (norm_bwd ? 2 * kRopeBwdSteps * step_bytes + warps * (int)D * 4
+                                      : kRopeFwdSteps * step_bytes);
     if (!norm_bwd) {
       rope_chunks(T, (int)(heads[0] + heads[1]), step, &p.chunks[0], &p.heads_per_chunk[0]);
       grid = (T * p.chunks[0] + warps - 1) / warps;

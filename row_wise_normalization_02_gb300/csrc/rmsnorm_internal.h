@@ -260,12 +260,16 @@ struct RopeKey {
   bool bwd;        // backward with the norm
   bool norm;
   bool adjacent;   // pairs (2i, 2i + 1); else (i, i + R / 2)
-  int g;           // lanes per row, 0: the scalar kernel
+  int e;           // elements per vector, 0: the scalar kernel
+  int g;           // lanes per row
+  int l;           // units (pairs of vectors) per lane
 };
 RopeKernel get_rope_kernel_f32_f32(const RopeKey& k);
 RopeKernel get_rope_kernel_bf16_bf16(const RopeKey& k);
 RopeKernel get_rope_kernel_bf16_f32(const RopeKey& k);
 constexpr int kRopeThreads = 256;
+constexpr int kRopeFwdSteps = 4;   // steps of rows in a thread's ring
+constexpr int kRopeBwdSteps = 3;
 
 // ---------------------------------------------------------------- token losses
 

@@ -243,6 +243,17 @@ def test_layouts(layout, offset, in_place):
 
 
 @gpu
+@pytest.mark.parametrize("xd,norm", [("bf16", True), ("f32", True), ("bf16", False)])
+@pytest.mark.parametrize("pairs", ["halves", "adjacent"])
+@pytest.mark.parametrize("D,R,offset", [
+    (80, 40, 0), (36, 36, 0), (36, 18, 0), (250, 250, 0), (250, 2, 0), (128, 128, 1), (256, 256, 1),
+    (256, 128, 2), (258, 258, 0), (512, 256, 4), (512, 512, 2), (130, 66, 3), (1024, 1024, 4),
+    (1030, 1030, 0)])
+def test_vectors_below_sixteen_bytes(D, R, offset, pairs, xd, norm):
+    check_case(Case(23, 5, 3, D, R, S3(R), pairs, "interleaved", xd, None, norm, "apart", offset))
+
+
+@gpu
 def test_many_tokens_and_heads():
     check_case(Case(5000, 6, 2, 64, 64, [12, 10, 10], order="interleaved"))
     check_case(Case(2, 300, 7, 128, 128, [24, 20, 20]))
