@@ -364,7 +364,7 @@ typedef struct rmsnorm_rope {
  * T < 2^30, Hq + Hk <= 2^16.  The kernels work in vectors of 16 bytes where
  * starts and strides are multiples of that and D and R of two of them, of 8, 4
  * or 2 bytes otherwise; rows beyond 64 vectors of 16 bytes or 256 smaller ones
- * take a scalar kernel.
+ * (128 of 8 bytes of bf16 in the backward) take smaller vectors or a scalar kernel.
  */
 rmsnorm_status_t rmsnorm_rope_fwd(const rmsnorm_heads_t* q, const rmsnorm_heads_t* k,
                                   const void* q_gamma, const void* k_gamma,

@@ -1697,19 +1697,20 @@ int view_alignment(const rmsnorm_heads_t& v, int64_t T, int es) {
 }
 
 // Shape of the vectorised kernels for operands aligned to `align` bytes: the
-// largest vectors that rows and halves divide into, G lanes of L units (two
-// vectors) per row.  All zero: the scalar kernel (rows beyond 64 such vectors of
-// 16 bytes or 256 smaller ones).
-void rope_shape(int64_t D, int64_t R, int xd, int align, int* e_out, int* g_out, int* l_out) {
+// largest vectors that rows and halves divide into and whose kernels reach that
+// far, G lanes of L units (two vectors) per row.  All zero: the scalar kernel.
+void rope_shape(int64_t D, int64_t R, int xd, int align, bool norm_bwd, int* e_out, int* g_out,
+                int* l_out) {
   *e_out = *g_out = *l_out = 0;
   const int full = per_vec(xd);
   for (int e = align / esize(xd); e > 0; e /= 2) {
     if (D % (2 * e) || R % (2 * e)) continue;
     const int64_t units = D / (2 * e);
-    int g = e == full ? 4 : 16, l = 1;
-    while (g < 32 && g < units) g *= 2;
-    while (e < full && l < 4 && (int64_t)g * l < units) l *= 2;
-    if ((int64_t)g * l < units) return;
+    const int per_lane = e == full ? 1 : norm_bwd && e == 4 ? 2 : 4;
+    int g = 4;
+    while (g < 32 && g * per_lane < units) g *= 2;
+    const int l = per_lane == 4 && 3 * g >= units ? 3 : per_lane;
+    if ((int64_t)g * l < units) continue;
     *e_out = e;
     *g_out = g;
     *l_out = l;
@@ -1721,6 +1722,7 @@ void rope_shape(int64_t D, int64_t R, int xd, int align, int* e_out, int* g_out,
 // the SMs (kRopeItems of them when the rows allow), each of whole steps of
 // `step` rows.
 constexpr int64_t kRopeItems = 4096;
+constexpr int kRopeBlockSteps = 8;
 void rope_chunks(int64_t T, int rows, int step, int* chunks, int* per_chunk) {
   const int64_t steps = (rows + step - 1) / step;
   int64_t c = T > 0 ? (kRopeItems + T - 1) / T : 1;
@@ -1847,11 +1849,7 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
   const int64_t R = rope->rotary_dim;
   const bool norm_bwd = bwd && norm;
   int e_vec, g, l;
-  rope_shape(D, R, xd, align, &e_vec, &g, &l);
-  const RopeKernel fn =
-      rope_kernel(RopeKey{xd, wd, norm_bwd, norm, rope->pairs == 1, e_vec, g, l});
-  if (!fn) return RMSNORM_ERR_INVALID_ARG;
-
+  rope_shape(D, R, xd, align, norm_bwd, &e_vec, &g, &l);
   RopeParams p = {};
   for (int i = 0; i < 2; ++i) {
     if (heads[i] == 0) continue;
@@ -1885,22 +1883,34 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
   p.ld_half = round_up((int)D, 4);
   p.partial = sums ? static_cast<float*>(workspace) : nullptr;
 
-  const int angles = (int)(R / 2 + 1) / 2 * 2 * 8;   // one token's table, bytes
   int64_t grid;
   int threads = kRopeThreads, smem;
+  p.block = 1;
   if (g > 0) {
     const int step = 32 / g, warps = kRopeThreads / 32;
+    // Tokens per work item: where a token's rows are fewer than kRopeBlockSteps
+    // steps (in the backward: those of its longer view), so many that an item has
+    // that many -- its lanes full, its start-up shared -- as long as kRopeItems items
+    // remain and a warp's angles stay below 2 KB.
+    const int64_t most = norm_bwd ? (heads[0] > heads[1] ? heads[0] : heads[1])
+                                  : heads[0] + heads[1];
+    while (l == 1 && p.block < kRopeMaxBlock && p.block * most < kRopeBlockSteps * step &&
+           T >= 2 * p.block * kRopeItems && p.block * R <= 256)
+      p.block *= 2;
+    const int64_t groups = (T + p.block - 1) / p.block;
+    const int half2 = (int)(R / 2 + 1) / 2 * 2, d4 = round_up((int)D, 4);
+    const int tables = warps * p.block * half2 * 8 + half2 * 8 + half2;
     const int step_bytes = 2 * l * e_vec * es * kRopeThreads;   // of one operand
-    smem = warps * angles + (norm_bwd ? 2 * kRopeBwdSteps * step_bytes + warps * (int)D * 4
-                                      : kRopeFwdSteps * step_bytes);
+    smem = tables + (norm_bwd ? 2 * kRopeBwdSteps * step_bytes + warps * d4 * 4
+                              : kRopeFwdSteps * step_bytes);
     if (!norm_bwd) {
-      rope_chunks(T, (int)(heads[0] + heads[1]), step, &p.chunks[0], &p.heads_per_chunk[0]);
-      grid = (T * p.chunks[0] + warps - 1) / warps;
+      rope_chunks(groups, (int)(heads[0] + heads[1]), step, &p.chunks[0], &p.heads_per_chunk[0]);
+      grid = (groups * p.chunks[0] + warps - 1) / warps;
     } else {
       int64_t items = 0;
       for (int i = 0; i < 2; ++i) {
-        rope_chunks(T, (int)heads[i], step, &p.chunks[i], &p.heads_per_chunk[i]);
-        if (heads[i]) items += T * p.chunks[i];
+        rope_chunks(groups, (int)heads[i], step, &p.chunks[i], &p.heads_per_chunk[i]);
+        if (heads[i]) items += groups * p.chunks[i];
       }
       grid = (items + warps - 1) / warps;
       if (grid > 2 * di.sms) grid = 2 * di.sms;
@@ -1918,6 +1928,9 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
     const int64_t cap = norm_bwd ? ctas : (int64_t)di.sms * 32;
     grid = items < cap ? items : cap;
   }
+  const RopeKernel fn = rope_kernel(
+      RopeKey{xd, wd, norm_bwd, norm, rope->pairs == 1, e_vec, g, l, p.block > 1});
+  if (!fn) return RMSNORM_ERR_INVALID_ARG;
   if ((e = ensure_smem(reinterpret_cast<const void*>(fn), dev, smem)) != cudaSuccess) {
     cudaGetLastError();
     return cuda_fail(e, "shared memory of the rotary kernel");

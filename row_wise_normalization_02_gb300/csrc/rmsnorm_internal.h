@@ -251,6 +251,7 @@ struct RopeParams {
   float eps, inv_d;
   int chunks[2];             // work items per token: chunks of heads_per_chunk heads (forward:
   int heads_per_chunk[2];    //   [0] covers the rows of q and k together)
+  int block;                 // or, where rows are few, tokens per work item (one chunk)
   float* partial;            // backward with the norm: [gridDim.x][2 * ld_half], or null
   int ld_half;
 };
@@ -263,6 +264,7 @@ struct RopeKey {
   int e;           // elements per vector, 0: the scalar kernel
   int g;           // lanes per row
   int l;           // units (pairs of vectors) per lane
+  bool block;      // items of several tokens
 };
 RopeKernel get_rope_kernel_f32_f32(const RopeKey& k);
 RopeKernel get_rope_kernel_bf16_bf16(const RopeKey& k);
@@ -270,6 +272,7 @@ RopeKernel get_rope_kernel_bf16_f32(const RopeKey& k);
 constexpr int kRopeThreads = 256;
 constexpr int kRopeFwdSteps = 4;   // steps of rows in a thread's ring
 constexpr int kRopeBwdSteps = 3;
+constexpr int kRopeMaxBlock = 8;   // tokens of one work item
 
 // ---------------------------------------------------------------- token losses
 

@@ -71,13 +71,17 @@ __device__ __forceinline__ int freq_axis(const RopeParams& p, int i) {
   return a;
 }
 
-// (cos, sign * sin) of frequency i at token t.
-__device__ __forceinline__ float2 angle(const RopeParams& p, int64_t t, int i) {
-  const int64_t pos = __ldg(p.positions + freq_axis(p, i) * p.pos_st + t);
-  const unsigned long long turn = (unsigned long long)pos * freq_turns(__ldg(p.inv_freq + i));
+// (cos, sign * sin) of a position times a frequency's turns.
+__device__ __forceinline__ float2 angle_of(long long pos, unsigned long long turns, float sign) {
+  const unsigned long long turn = (unsigned long long)pos * turns;
   float s, c;
   sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
-  return make_float2(c, p.sign * s);
+  return make_float2(c, sign * s);
+}
+// The same for frequency i at token t.
+__device__ __forceinline__ float2 angle(const RopeParams& p, int64_t t, int i) {
+  return angle_of(__ldg(p.positions + freq_axis(p, i) * p.pos_st + t),
+                  freq_turns(__ldg(p.inv_freq + i)), p.sign);
 }
 
 // Vectors of E elements: 16 bytes, or 8, 4 or 2 where rows, strides or halves do
@@ -88,70 +92,70 @@ template <> struct Raw<8> { uint2 v; };
 template <> struct Raw<4> { uint32_t v; };
 template <> struct Raw<2> { uint16_t v; };
 
-__device__ __forceinline__ void unpack_raw(const Raw<16>& r, float (&f)[4]) { unpack(r.v, f); }
-__device__ __forceinline__ void unpack_raw(const Raw<16>& r, float (&f)[8]) { unpack(r.v, f); }
-__device__ __forceinline__ void unpack_raw(const Raw<8>& r, float (&f)[2]) {
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<16>& r, float (&f)[4]) { unpack(r.v, f); }
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<16>& r, float (&f)[8]) { unpack(r.v, f); }
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<8>& r, float (&f)[2]) {
   f[0] = __uint_as_float(r.v.x);
   f[1] = __uint_as_float(r.v.y);
 }
-__device__ __forceinline__ void unpack_raw(const Raw<8>& r, float (&f)[4]) {
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<8>& r, float (&f)[4]) {
   unpack_word_bf16(r.v.x, f[0], f[1]);
   unpack_word_bf16(r.v.y, f[2], f[3]);
 }
-__device__ __forceinline__ void unpack_raw(const Raw<4>& r, float (&f)[1]) {
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<4>& r, float (&f)[1]) {
   f[0] = __uint_as_float(r.v);
 }
-__device__ __forceinline__ void unpack_raw(const Raw<4>& r, float (&f)[2]) {
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<4>& r, float (&f)[2]) {
   unpack_word_bf16(r.v, f[0], f[1]);
 }
-__device__ __forceinline__ void unpack_raw(const Raw<2>& r, float (&f)[1]) {
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<2>& r, float (&f)[1]) {
   f[0] = __uint_as_float((uint32_t)r.v << 16);
 }
 
 // Streaming stores of a vector.
-__device__ __forceinline__ void store_vec(void* p, const float (&f)[8], bf16*) {
+[[maybe_unused]] __device__ __forceinline__ void store_vec(void* p, const float (&f)[8], bf16*) {
   st_stream(p, pack(f));
 }
-__device__ __forceinline__ void store_vec(void* p, const float (&f)[4], float*) {
+[[maybe_unused]] __device__ __forceinline__ void store_vec(void* p, const float (&f)[4], float*) {
   st_stream(p, pack(f));
 }
-__device__ __forceinline__ void store_words(void* p, uint32_t a, uint32_t b) {
+[[maybe_unused]] __device__ __forceinline__ void store_words(void* p, uint32_t a, uint32_t b) {
   asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(a), "r"(b) : "memory");
 }
-__device__ __forceinline__ void store_word(void* p, uint32_t a) {
+[[maybe_unused]] __device__ __forceinline__ void store_word(void* p, uint32_t a) {
   asm volatile("st.global.cs.u32 [%0], %1;" ::"l"(p), "r"(a) : "memory");
 }
-__device__ __forceinline__ void store_vec(void* p, const float (&f)[4], bf16*) {
+[[maybe_unused]] __device__ __forceinline__ void store_vec(void* p, const float (&f)[4], bf16*) {
   store_words(p, pack_word_bf16(f[0], f[1]), pack_word_bf16(f[2], f[3]));
 }
-__device__ __forceinline__ void store_vec(void* p, const float (&f)[2], bf16*) {
+[[maybe_unused]] __device__ __forceinline__ void store_vec(void* p, const float (&f)[2], bf16*) {
   store_word(p, pack_word_bf16(f[0], f[1]));
 }
-__device__ __forceinline__ void store_vec(void* p, const float (&f)[1], bf16*) {
+[[maybe_unused]] __device__ __forceinline__ void store_vec(void* p, const float (&f)[1], bf16*) {
   st_scalar(static_cast<bf16*>(p), f[0]);
 }
-__device__ __forceinline__ void store_vec(void* p, const float (&f)[2], float*) {
+[[maybe_unused]] __device__ __forceinline__ void store_vec(void* p, const float (&f)[2], float*) {
   store_words(p, __float_as_uint(f[0]), __float_as_uint(f[1]));
 }
-__device__ __forceinline__ void store_vec(void* p, const float (&f)[1], float*) {
+[[maybe_unused]] __device__ __forceinline__ void store_vec(void* p, const float (&f)[1], float*) {
   store_word(p, __float_as_uint(f[0]));
 }
 
 // Global -> shared copy of one vector, which the copying thread reads back itself
 // after copy_wait: no barrier.  (Two bytes have no asynchronous form.)
-__device__ __forceinline__ void copy_vec(Raw<16>* dst, const void* src) {
+[[maybe_unused]] __device__ __forceinline__ void copy_vec(Raw<16>* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void copy_vec(Raw<8>* dst, const void* src) {
+[[maybe_unused]] __device__ __forceinline__ void copy_vec(Raw<8>* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void copy_vec(Raw<4>* dst, const void* src) {
+[[maybe_unused]] __device__ __forceinline__ void copy_vec(Raw<4>* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void copy_vec(Raw<2>* dst, const void* src) {
+[[maybe_unused]] __device__ __forceinline__ void copy_vec(Raw<2>* dst, const void* src) {
   dst->v = *static_cast<const volatile uint16_t*>(src);
 }
 __device__ __forceinline__ void copy_commit() {
@@ -178,12 +182,18 @@ __device__ __forceinline__ Raw<B> slot_of(const Raw<B>* p) {
   return r;
 }
 
-// The two vectors of unit u of a row (see the note at the top): rotary units
-// first, then the unrotated columns two neighbours at a time.
+// The two vectors of unit u of a row, such that every pair is within the unit and
+// lanes next to each other read next to each other.  Halves: vector u of the first
+// half of the rotated columns and vector u of the second; behind them the others,
+// two neighbours at a time.  Adjacent pairs lie within a vector: vectors u and u +
+// units.  Single elements in adjacent pairs: 2u and 2u + 1.
 template <int E, bool ADJ>
 __device__ __forceinline__ void unit_vectors(const RopeParams& p, int u, int* a, int* b) {
   const int half = p.R / (2 * E);
-  if (ADJ || u >= half) {
+  if (ADJ && E > 1) {
+    *a = u;
+    *b = u + p.D / (2 * E);
+  } else if (ADJ || u >= half) {
     *a = 2 * u;
     *b = 2 * u + 1;
   } else {
@@ -192,21 +202,108 @@ __device__ __forceinline__ void unit_vectors(const RopeParams& p, int u, int* a,
   }
 }
 
+// Operations on pairs of registers, E / 2 at a time (E = 1: one).
+__device__ __forceinline__ float2 pair_at(const float* a, int i) { return make_float2(a[i], a[i + 1]); }
+__device__ __forceinline__ void put_pair(float* a, int i, float2 v) {
+  a[i] = v.x;
+  a[i + 1] = v.y;
+}
+// o = a * b
+template <int E>
+__device__ __forceinline__ void mul_all(float (&o)[E], const float (&a)[E], const float (&b)[E]) {
+  if constexpr (E == 1) o[0] = a[0] * b[0];
+#pragma unroll
+  for (int i = 0; i + 1 < E; i += 2) put_pair(o, i, __fmul2_rn(pair_at(a, i), pair_at(b, i)));
+}
+// o = a * s
+template <int E>
+__device__ __forceinline__ void scale_all(float (&o)[E], const float (&a)[E], float s) {
+  if constexpr (E == 1) o[0] = a[0] * s;
+#pragma unroll
+  for (int i = 0; i + 1 < E; i += 2) put_pair(o, i, __fmul2_rn(pair_at(a, i), make_float2(s, s)));
+}
+// o += a * b
+template <int E>
+__device__ __forceinline__ void fma_all(float (&o)[E], const float (&a)[E], const float (&b)[E]) {
+  if constexpr (E == 1) o[0] = fmaf(a[0], b[0], o[0]);
+#pragma unroll
+  for (int i = 0; i + 1 < E; i += 2)
+    put_pair(o, i, __ffma2_rn(pair_at(a, i), pair_at(b, i), pair_at(o, i)));
+}
+// o += a * s
+template <int E>
+__device__ __forceinline__ void axpy_all(float (&o)[E], const float (&a)[E], float s) {
+  if constexpr (E == 1) o[0] = fmaf(a[0], s, o[0]);
+#pragma unroll
+  for (int i = 0; i + 1 < E; i += 2)
+    put_pair(o, i, __ffma2_rn(pair_at(a, i), make_float2(s, s), pair_at(o, i)));
+}
+// Two running sums of a * b.
+template <int E>
+__device__ __forceinline__ void dot_all(float2& acc, const float (&a)[E], const float (&b)[E]) {
+  if constexpr (E == 1) acc.x = fmaf(a[0], b[0], acc.x);
+#pragma unroll
+  for (int i = 0; i + 1 < E; i += 2) acc = __ffma2_rn(pair_at(a, i), pair_at(b, i), acc);
+}
+
+// The cosines and sines of a unit's pairs.
+template <int E>
+struct Turn {
+  float c[E], s[E];
+};
+
 // Rotate the E pairs a unit holds: halves pair a[i] with b[i], adjacent pairs
 // lie side by side in a, then in b (single elements: a with b again).
 template <int E, bool ADJ>
-__device__ __forceinline__ void rotate(float (&a)[E], float (&b)[E], const float2 (&cs)[E]) {
+__device__ __forceinline__ void rotate(float (&a)[E], float (&b)[E], const Turn<E>& t) {
+  if constexpr (ADJ && E > 1) {
+    // (u, v) -> u (c, s) + v (-s, c)
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    constexpr bool kSide = ADJ && E > 1;
-    float* u = kSide ? (i < E / 2 ? &a[2 * i] : &b[2 * i - E]) : &a[i];
-    float* v = kSide ? u + 1 : &b[i];
-    const float x = *u, y = *v;
-    *u = x * cs[i].x - y * cs[i].y;
-    *v = x * cs[i].y + y * cs[i].x;
+    for (int i = 0; i < E; ++i) {
+      float* u = i < E / 2 ? &a[2 * i] : &b[2 * i - E];
+      const float2 p = __fmul2_rn(make_float2(u[1], u[1]), make_float2(-t.s[i], t.c[i]));
+      put_pair(u, 0, __ffma2_rn(make_float2(u[0], u[0]), make_float2(t.c[i], t.s[i]), p));
+    }
+  } else {
+    float n[E], x[E], y[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) n[i] = -t.s[i];
+    mul_all(x, b, n);
+    mul_all(y, a, t.s);
+    fma_all(x, a, t.c);
+    fma_all(y, b, t.c);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      a[i] = x[i];
+      b[i] = y[i];
+    }
   }
 }
 
+// What a CTA of the vectorised kernels keeps in shared memory behind its ring: the
+// frequencies as turns and their axes, and each warp's cosines and sines for the
+// tokens it is at.
+struct Tables {
+  unsigned long long* turns;   // [R / 2]
+  float2* angles;              // the warp's, [block][R / 2 rounded to 2]
+  uint8_t* axis;               // [R / 2]
+  int ld_angles;
+};
+__device__ __forceinline__ Tables make_tables(const RopeParams& p, void* at) {
+  Tables t;
+  const int half = p.R / 2, warps = kRopeThreads / 32;
+  t.ld_angles = (half + 1) & ~1;
+  t.angles = static_cast<float2*>(at);
+  t.turns = reinterpret_cast<unsigned long long*>(t.angles + warps * p.block * t.ld_angles);
+  t.axis = reinterpret_cast<uint8_t*>(t.turns + t.ld_angles);
+  t.angles += (threadIdx.x >> 5) * p.block * t.ld_angles;
+  for (int i = threadIdx.x; i < half; i += kRopeThreads) {
+    t.turns[i] = freq_turns(__ldg(p.inv_freq + i));
+    t.axis[i] = (uint8_t)freq_axis(p, i);
+  }
+  __syncthreads();
+  return t;
+}
 template <typename TX, typename TW, int E>
 __device__ __forceinline__ void load_gamma(const void* gamma, int vec, float (&w)[E]) {
   const TW* g = static_cast<const TW*>(gamma) + (size_t)vec * E;
@@ -227,42 +324,63 @@ __device__ __forceinline__ void load_gamma(const void* gamma, int vec, float (&w
   }
 }
 
-template <int E>
-__device__ __forceinline__ float sum_sq(const float (&a)[E], const float (&b)[E]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
-  return s;
+// Lane 4 k + a holds the position of token t0 + k on axis a (of up to eight
+// tokens), so that it can be asked for long before it is needed.
+__device__ __forceinline__ long long lane_position(const RopeParams& p, int64_t t0, int tokens) {
+  const int lane = threadIdx.x & 31, k = lane >> 2, a = lane & 3;
+  return k < tokens && a < p.axes ? __ldg(p.positions + a * p.pos_st + t0 + k) : 0;
 }
-
-// The warp's angles of token t, one frequency per lane and step ...
-__device__ __forceinline__ void warp_angles(const RopeParams& p, int64_t t, float2* table) {
-  __syncwarp();   // the previous token's readers are done
-  for (int i = threadIdx.x & 31; i < p.R / 2; i += 32) table[i] = angle(p, t, i);
+// The warp's angles of those tokens, one frequency per lane and step ...
+__device__ __forceinline__ void warp_angles(const RopeParams& p, const Tables& tab, long long pos,
+                                            int tokens) {
+  const int lane = threadIdx.x & 31, half = p.R / 2;
+  __syncwarp();   // the previous tokens' readers are done
+  for (int k = 0; k < tokens; ++k)
+    for (int i0 = 0; i0 < half; i0 += 32) {
+      const int i = i0 + lane;
+      const long long at = __shfl_sync(0xFFFFFFFFu, pos, 4 * k + (i < half ? tab.axis[i] : 0));
+      if (i < half) tab.angles[k * tab.ld_angles + i] = angle_of(at, tab.turns[i], p.sign);
+    }
   __syncwarp();
 }
-// ... and a unit's E of them.
-template <int E>
-__device__ __forceinline__ void unit_angles(const float2* table, int u, bool rotary,
-                                            float2 (&cs)[E]) {
-  if constexpr (E == 1) {
-    cs[0] = rotary ? table[u] : make_float2(1.f, 0.f);
+// ... and a unit's E of them (adjacent pairs: those of its first vector, then those
+// of its second), no turn for columns from R on.
+template <int N>
+__device__ __forceinline__ void read_angles(const float2* table, bool rotary, float* c, float* s) {
+  if constexpr (N == 1) {
+    const float2 q = rotary ? table[0] : make_float2(1.f, 0.f);
+    c[0] = q.x;
+    s[0] = q.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const float4 q = rotary ? *reinterpret_cast<const float4*>(table + u * E + i)
+    for (int i = 0; i < N; i += 2) {
+      const float4 q = rotary ? *reinterpret_cast<const float4*>(table + i)
                               : make_float4(1.f, 0.f, 1.f, 0.f);
-      cs[i] = make_float2(q.x, q.y);
-      cs[i + 1] = make_float2(q.z, q.w);
+      c[i] = q.x;
+      s[i] = q.y;
+      c[i + 1] = q.z;
+      s[i + 1] = q.w;
     }
+  }
+}
+template <int E, bool ADJ>
+__device__ __forceinline__ void unit_angles(const RopeParams& p, const float2* table, int u,
+                                            Turn<E>& t) {
+  if constexpr (ADJ && E > 1) {
+    const int v = u + p.D / (2 * E);
+    read_angles<E / 2>(table + u * (E / 2), u < p.R / E, t.c, t.s);
+    read_angles<E / 2>(table + v * (E / 2), v < p.R / E, t.c + E / 2, t.s + E / 2);
+  } else {
+    read_angles<E>(table + u * E, u < p.R / (2 * E), t.c, t.s);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Forward, and the backward of the rotation alone (sign -1).  One warp per
-// (token, chunk of rows); q's rows come first, k's follow.  A row is G lanes of L
-// units; steps of 32 / G rows go through a ring of S steps per thread.
-template <typename TX, typename TW, int E, int G, int L, bool NORM, bool ADJ>
+// Forward, and the backward of the rotation alone (sign -1).  A warp takes one
+// token, or a chunk of its rows where tokens are few, or a block of tokens where
+// rows are; a token's rows are q's, then k's.  A row is G lanes of L units; steps of
+// 32 / G rows go through a ring of S steps per thread.
+template <typename TX, typename TW, int E, int G, int L, bool NORM, bool ADJ, bool BLOCK>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
   constexpr int RG = 32 / G, B = E * sizeof(TX), S = kRopeFwdSteps;
   using V = Raw<B>;
@@ -271,28 +389,38 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane % G, rg = lane / G;
   V* ring = reinterpret_cast<V*>(smem4) + tid;   // [S][2 L][threads]
-  float2* table = reinterpret_cast<float2*>(reinterpret_cast<V*>(smem4) +
-                                            S * 2 * L * kRopeThreads) +
-                  warp * ((p.R / 2 + 1) & ~1);
   const uint32_t item = blockIdx.x * (kRopeThreads / 32) + warp;
-  const uint32_t t32 = item / (uint32_t)p.chunks[0];
-  const int64_t t = t32;
-  if (t >= p.T) return;
-  const int h0 = (int)(item - t32 * (uint32_t)p.chunks[0]) * p.heads_per_chunk[0];
-  const int nq = p.v[0].heads, rows = nq + p.v[1].heads;
-  const int h1 = min(h0 + p.heads_per_chunk[0], rows);
+  const uint32_t group = item / (uint32_t)p.chunks[0];   // block of tokens
+  const int64_t t0 = (int64_t)group * (BLOCK ? p.block : 1);
+  const int tokens = (int)max((int64_t)0, min((int64_t)(BLOCK ? p.block : 1), p.T - t0));
+  const int h0 = (int)(item - group * (uint32_t)p.chunks[0]) * p.heads_per_chunk[0];
+  const int nq = p.v[0].heads, all = nq + p.v[1].heads;
+  const int rows = min(p.heads_per_chunk[0], all - h0);   // of each token
+  const int total = tokens * rows;
   const int units = p.D / (2 * E);
   int va[L], vb[L];
 #pragma unroll
   for (int k = 0; k < L; ++k) unit_vectors<E, ADJ>(p, g + k * G, &va[k], &vb[k]);
-  const TX* xq = static_cast<const TX*>(p.v[0].x) + t * p.v[0].x_st;
-  const TX* xk = static_cast<const TX*>(p.v[1].x) + t * p.v[1].x_st;
-  TX* yq = static_cast<TX*>(p.v[0].y) + t * p.v[0].y_st;
-  TX* yk = static_cast<TX*>(p.v[1].y) + t * p.v[1].y_st;
 
-  auto load = [&](int stage, int r) {
-    if (r < h1) {
+  // row j of the item: head r of token t0 + k
+  auto place = [&](int j, int* k, int* r) {
+    *k = 0;
+    *r = h0 + j;
+    if (BLOCK) {
+      *k = j / rows;
+      *r -= *k * rows;
+    }
+  };
+  const TX* xq = static_cast<const TX*>(p.v[0].x) + t0 * p.v[0].x_st;
+  const TX* xk = static_cast<const TX*>(p.v[1].x) + t0 * p.v[1].x_st;
+  TX* yq = static_cast<TX*>(p.v[0].y) + t0 * p.v[0].y_st;
+  TX* yk = static_cast<TX*>(p.v[1].y) + t0 * p.v[1].y_st;
+  auto load = [&](int stage, int j) {
+    if (j < total) {
+      int tok, r;
+      place(j, &tok, &r);
       const TX* x = r < nq ? xq + r * p.v[0].x_sh : xk + (r - nq) * p.v[1].x_sh;
+      if (BLOCK) x += tok * (r < nq ? p.v[0].x_st : p.v[1].x_st);
       V* slot = ring + stage * (2 * L * kRopeThreads);
 #pragma unroll
       for (int k = 0; k < L; ++k)
@@ -303,47 +431,67 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
     }
     copy_commit();
   };
+  // the first rows are on their way while the angles are computed
 #pragma unroll
-  for (int s = 0; s < S; ++s) load(s, h0 + s * RG + rg);   // on their way while the angles are computed
-  warp_angles(p, t, table);
-  float2 cs[L][E];
+  for (int s = 0; s < S; ++s) load(s, s * RG + rg);
+  const long long pos = lane_position(p, t0, tokens);
+  const Tables tab =
+      make_tables(p, reinterpret_cast<V*>(smem4) + S * 2 * L * kRopeThreads);
+  warp_angles(p, tab, pos, tokens);
+  Turn<E> cs[L];
+  auto angles_at = [&](int tok) {
 #pragma unroll
-  for (int k = 0; k < L; ++k)
-    unit_angles<E>(table, g + k * G, g + k * G < p.R / (2 * E), cs[k]);
+    for (int k = 0; k < L; ++k)
+      unit_angles<E, ADJ>(p, tab.angles + tok * tab.ld_angles, g + k * G, cs[k]);
+  };
+  int at = -1;   // the token whose angles cs holds
+  if (!BLOCK) angles_at(0);
   int stage = 0;
-  for (int r0 = h0; r0 < h1; r0 += RG) {
-    const int r = r0 + rg;
+  for (int j0 = 0; j0 < total; j0 += RG) {
+    const int j = j0 + rg;
+    int tok, r;
+    place(j, &tok, &r);
+    const bool live = j < total;
+    if (BLOCK && live && tok != at) {
+      at = tok;
+      angles_at(tok);
+    }
     copy_wait<S - 1>();
     const V* slot = ring + stage * (2 * L * kRopeThreads);
-    float a[L][E], b[L][E], ss = 0.f;
+    float a[L][E], b[L][E];
+    float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < L; ++k) {
-      if (r < h1 && g + k * G < units) {
+      if (live && g + k * G < units) {
         unpack_raw(slot_of(slot + 2 * k * kRopeThreads), a[k]);
         unpack_raw(slot_of(slot + (2 * k + 1) * kRopeThreads), b[k]);
       } else {
 #pragma unroll
         for (int i = 0; i < E; ++i) a[k][i] = b[k][i] = 0.f;
       }
-      if (NORM) ss += sum_sq(a[k], b[k]);
+      if (NORM) {
+        dot_all(ss, a[k], a[k]);
+        dot_all(ss, b[k], b[k]);
+      }
     }
-    load(stage, r + S * RG);
+    load(stage, j + S * RG);
     stage = stage + 1 == S ? 0 : stage + 1;
-    if (NORM) ss = rsqrtf(group_sum<G>(ss) * p.inv_d + p.eps);
-    if (r >= h1) continue;
+    float rstd = 1.f;
+    if (NORM) rstd = rsqrtf(group_sum<G>(ss.x + ss.y) * p.inv_d + p.eps);
+    if (!live) continue;
     TX* y = r < nq ? yq + r * p.v[0].y_sh : yk + (r - nq) * p.v[1].y_sh;
+    if (BLOCK) y += tok * (r < nq ? p.v[0].y_st : p.v[1].y_st);
 #pragma unroll
     for (int k = 0; k < L; ++k) {
       if (g + k * G >= units) continue;
-      if (NORM) {
-        const void* gamma = r < nq ? p.v[0].gamma : p.v[1].gamma;
+      if (NORM) {   // gamma from L1: in registers it would cost a CTA per SM (116 us for 105)
         float w[E];
-        load_gamma<TX, TW>(gamma, va[k], w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) a[k][i] *= ss * w[i];
-        load_gamma<TX, TW>(gamma, vb[k], w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) b[k][i] *= ss * w[i];
+        load_gamma<TX, TW>(r < nq ? p.v[0].gamma : p.v[1].gamma, va[k], w);
+        scale_all(w, w, rstd);
+        mul_all(a[k], a[k], w);
+        load_gamma<TX, TW>(r < nq ? p.v[0].gamma : p.v[1].gamma, vb[k], w);
+        scale_all(w, w, rstd);
+        mul_all(b[k], b[k], w);
       }
       rotate<E, ADJ>(a[k], b[k], cs[k]);
       store_vec(y + va[k] * E, a[k], static_cast<TX*>(nullptr));
@@ -353,11 +501,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Backward with the norm.  Persistent: each warp walks (token, chunk) items of
-// q, then those of k, its lanes keeping the dgamma partials of their columns
-// in registers; after each view the CTA adds its lanes' partials in a fixed
-// order into its partial row.
-template <typename TX, typename TW, int E, int G, int L, bool ADJ>
+// Backward with the norm.  Persistent: each warp walks items (a token, a chunk of
+// its rows, or a block of tokens) of q, then those of k, its lanes keeping the
+// dgamma partials of their columns in registers; after each view the CTA adds its
+// lanes' partials in a fixed order into its partial row.  The ring runs on from
+// item to item, and so do the positions, one item ahead.
+template <typename TX, typename TW, int E, int G, int L, bool ADJ, bool BLOCK>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopeParams p) {
   constexpr int RG = 32 / G, W = kRopeThreads / 32, B = E * sizeof(TX), S = kRopeBwdSteps;
   using V = Raw<B>;
@@ -370,11 +519,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
 #pragma unroll
   for (int k = 0; k < L; ++k) unit_vectors<E, ADJ>(p, g + k * G, &va[k], &vb[k]);
   V* ring = reinterpret_cast<V*>(smem4) + tid;                        // [S][4 L][threads]
-  float2* tables = reinterpret_cast<float2*>(reinterpret_cast<V*>(smem4) +
-                                             S * 4 * L * kRopeThreads);
-  float2* table = tables + warp * ((p.R / 2 + 1) & ~1);
-  float* red = reinterpret_cast<float*>(tables + W * ((p.R / 2 + 1) & ~1));   // [W][D]
+  float* red = reinterpret_cast<float*>(reinterpret_cast<V*>(smem4) +
+                                        S * 4 * L * kRopeThreads);    // [W][D rounded to 4]
+  const int ld_red = (p.D + 3) & ~3;
+  const Tables tab = make_tables(p, red + W * ld_red);
   const uint32_t nw = gridDim.x * W, w0 = blockIdx.x * W + warp;
+  const int block = BLOCK ? p.block : 1;
+  const uint32_t groups = (uint32_t)((p.T + block - 1) / block);
   uint32_t skip = 0;   // items of q, so that k's start where q's ended
 
   for (int side = 0; side < 2; ++side) {
@@ -386,7 +537,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
       continue;
     }
     const uint32_t chunks = (uint32_t)p.chunks[side];
-    const uint32_t items = (uint32_t)p.T * chunks;
+    const uint32_t items = groups * chunks;
     float wa[L][E], wb[L][E], ga[L][E], gb[L][E];
 #pragma unroll
     for (int k = 0; k < L; ++k) {
@@ -397,24 +548,42 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
         load_gamma<TX, TW>(v.gamma, vb[k], wb[k]);
       }
     }
-    // what comes next into the ring: a step of an item
-    uint32_t f_it = (w0 + nw - skip % nw) % nw;
-    int f_h = 0, f_h1 = 0;
-    const TX *f_x = nullptr, *f_dy = nullptr;
-    auto f_begin = [&]() {
-      if (f_it >= items) return;
-      const uint32_t t32 = f_it / chunks;
-      f_h = (int)(f_it - t32 * chunks) * p.heads_per_chunk[side];
-      f_h1 = min(f_h + p.heads_per_chunk[side], v.heads);
-      f_x = static_cast<const TX*>(v.x) + (int64_t)t32 * v.x_st;
-      f_dy = static_cast<const TX*>(v.dy) + (int64_t)t32 * v.dy_st;
+
+    // an item: tokens [t0, t0 + tokens), rows [h0, h0 + rows) of each
+    struct Item {
+      int64_t t0;
+      int tokens, h0, rows;
     };
+    auto item_at = [&](uint32_t it) {
+      const uint32_t group = it / chunks;
+      Item m;
+      m.t0 = (int64_t)group * block;
+      m.tokens = BLOCK ? (int)min((int64_t)block, p.T - m.t0) : 1;
+      m.h0 = (int)(it - group * chunks) * p.heads_per_chunk[side];
+      m.rows = min(p.heads_per_chunk[side], v.heads - m.h0);
+      return m;
+    };
+    auto place = [&](const Item& m, int j, int* k, int* h) {
+      *k = 0;
+      *h = m.h0 + j;
+      if (BLOCK) {
+        *k = j / m.rows;
+        *h -= *k * m.rows;
+      }
+    };
+    // what comes next into the ring: row f_j of item f
+    uint32_t it = (w0 + nw - skip % nw) % nw, f_it = it;
+    int f_j = 0;
+    Item f{};
+    if (f_it < items) f = item_at(f_it);
     auto load = [&](int stage) {
       if (f_it < items) {
-        const int h = f_h + rg;
-        if (h < f_h1) {
-          const TX* xr = f_x + h * v.x_sh;
-          const TX* dr = f_dy + h * v.dy_sh;
+        const int j = f_j + rg;
+        if (j < f.tokens * f.rows) {
+          int tok, h;
+          place(f, j, &tok, &h);
+          const TX* xr = static_cast<const TX*>(v.x) + (f.t0 + tok) * v.x_st + h * v.x_sh;
+          const TX* dr = static_cast<const TX*>(v.dy) + (f.t0 + tok) * v.dy_st + h * v.dy_sh;
           V* slot = ring + stage * (4 * L * kRopeThreads);
 #pragma unroll
           for (int k = 0; k < L; ++k)
@@ -425,75 +594,96 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
               copy_vec(slot + (4 * k + 3) * kRopeThreads, dr + vb[k] * E);
             }
         }
-        f_h += RG;
-        if (f_h >= f_h1) {
+        f_j += RG;
+        if (f_j >= f.tokens * f.rows) {
+          f_j = 0;
           f_it += nw;
-          f_begin();
+          if (f_it < items) f = item_at(f_it);
         }
       }
       copy_commit();
     };
-    uint32_t it = f_it;
-    f_begin();
+    long long pos = 0;
+    if (it < items) {
+      const Item m = item_at(it);
+      pos = lane_position(p, m.t0, m.tokens);
+    }
 #pragma unroll
     for (int s = 0; s < S; ++s) load(s);
     int stage = 0;
     for (; it < items; it += nw) {
-      const uint32_t t32 = it / chunks;
-      const int64_t t = t32;
-      const int h0 = (int)(it - t32 * chunks) * p.heads_per_chunk[side];
-      const int h1 = min(h0 + p.heads_per_chunk[side], v.heads);
-      TX* yt = static_cast<TX*>(v.y) + t * v.y_st;
-      warp_angles(p, t, table);
-      float2 cs[L][E];
+      const Item m = item_at(it);
+      warp_angles(p, tab, pos, m.tokens);
+      if (it + nw < items) {
+        const Item n = item_at(it + nw);
+        pos = lane_position(p, n.t0, n.tokens);
+      }
+      Turn<E> cs[L];
+      auto angles_at = [&](int tok) {
 #pragma unroll
-      for (int k = 0; k < L; ++k)
-        unit_angles<E>(table, g + k * G, g + k * G < p.R / (2 * E), cs[k]);
-      for (int hb = h0; hb < h1; hb += RG) {
-        const int h = hb + rg;
+        for (int k = 0; k < L; ++k)
+          unit_angles<E, ADJ>(p, tab.angles + tok * tab.ld_angles, g + k * G, cs[k]);
+      };
+      int at = -1;   // the token whose angles cs holds
+      if (!BLOCK) angles_at(0);
+      const int total = m.tokens * m.rows;
+      for (int j0 = 0; j0 < total; j0 += RG) {
+        const int j = j0 + rg;
+        int tok, h;
+        place(m, j, &tok, &h);
+        const bool live = j < total;
+        if (BLOCK && live && tok != at) {
+          at = tok;
+          angles_at(tok);
+        }
         copy_wait<S - 1>();
         const V* slot = ring + stage * (4 * L * kRopeThreads);
         float a[L][E], b[L][E], da[L][E], db[L][E];
-        float ss = 0.f, dot = 0.f;
+        float2 ss = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < L; ++k) {
-          if (h < h1 && g + k * G < units) {
+          if (live && g + k * G < units) {
             unpack_raw(slot_of(slot + 4 * k * kRopeThreads), a[k]);
             unpack_raw(slot_of(slot + (4 * k + 1) * kRopeThreads), b[k]);
             unpack_raw(slot_of(slot + (4 * k + 2) * kRopeThreads), da[k]);
             unpack_raw(slot_of(slot + (4 * k + 3) * kRopeThreads), db[k]);
+            rotate<E, ADJ>(da[k], db[k], cs[k]);
           } else {
 #pragma unroll
             for (int i = 0; i < E; ++i) a[k][i] = b[k][i] = da[k][i] = db[k][i] = 0.f;
           }
-          rotate<E, ADJ>(da[k], db[k], cs[k]);
-          ss += sum_sq(a[k], b[k]);
-#pragma unroll
-          for (int i = 0; i < E; ++i) {
-            dot = fmaf(wa[k][i] * da[k][i], a[k][i], dot);
-            dot = fmaf(wb[k][i] * db[k][i], b[k][i], dot);
-          }
+          dot_all(ss, a[k], a[k]);
+          dot_all(ss, b[k], b[k]);
         }
         load(stage);
         stage = stage + 1 == S ? 0 : stage + 1;
-        ss = group_sum<G>(ss);
-        dot = group_sum<G>(dot);
-        const float r = rsqrtf(ss * p.inv_d + p.eps);
-        const float c = r * r * p.inv_d * dot;
-        if (h >= h1) continue;
-        TX* y = yt + h * v.y_sh;
+        const float r = rsqrtf(group_sum<G>(ss.x + ss.y) * p.inv_d + p.eps);
+        // dgamma takes g x r; then g becomes g gamma
 #pragma unroll
         for (int k = 0; k < L; ++k) {
           if (g + k * G >= units) continue;
+          float x[E];
+          scale_all(x, a[k], r);
+          fma_all(ga[k], da[k], x);
+          mul_all(da[k], da[k], wa[k]);
+          dot_all(dot, da[k], a[k]);
+          scale_all(x, b[k], r);
+          fma_all(gb[k], db[k], x);
+          mul_all(db[k], db[k], wb[k]);
+          dot_all(dot, db[k], b[k]);
+        }
+        const float c = r * r * p.inv_d * group_sum<G>(dot.x + dot.y);
+        if (!live) continue;
+        TX* y = static_cast<TX*>(v.y) + (m.t0 + tok) * v.y_st + h * v.y_sh;
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            ga[k][i] = fmaf(da[k][i] * a[k][i], r, ga[k][i]);
-            gb[k][i] = fmaf(db[k][i] * b[k][i], r, gb[k][i]);
-            a[k][i] = r * fmaf(-a[k][i], c, wa[k][i] * da[k][i]);
-            b[k][i] = r * fmaf(-b[k][i], c, wb[k][i] * db[k][i]);
-          }
-          store_vec(y + va[k] * E, a[k], static_cast<TX*>(nullptr));
-          store_vec(y + vb[k] * E, b[k], static_cast<TX*>(nullptr));
+        for (int k = 0; k < L; ++k) {
+          if (g + k * G >= units) continue;
+          axpy_all(da[k], a[k], -c);
+          scale_all(da[k], da[k], r);
+          axpy_all(db[k], b[k], -c);
+          scale_all(db[k], db[k], r);
+          store_vec(y + va[k] * E, da[k], static_cast<TX*>(nullptr));
+          store_vec(y + vb[k] * E, db[k], static_cast<TX*>(nullptr));
         }
       }
     }
@@ -510,8 +700,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
             gb[k][i] += __shfl_xor_sync(0xFFFFFFFFu, gb[k][i], o);
           }
           if (g + k * G < units && rg == 0) {
-            red[warp * p.D + va[k] * E + i] = ga[k][i];
-            red[warp * p.D + vb[k] * E + i] = gb[k][i];
+            red[warp * ld_red + va[k] * E + i] = ga[k][i];
+            red[warp * ld_red + vb[k] * E + i] = gb[k][i];
           }
         }
       }
@@ -519,7 +709,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
       for (int d = tid; d < p.ld_half; d += kRopeThreads) {
         float s = 0.f;
         if (d < p.D)
-          for (int w = 0; w < W; ++w) s += red[w * p.D + d];
+          for (int w = 0; w < W; ++w) s += red[w * ld_red + d];
         p.partial[(size_t)blockIdx.x * 2 * p.ld_half + side * p.ld_half + d] = s;
       }
     }
@@ -642,54 +832,64 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(RopeParams p)
 
 // ---------------------------------------------------------------------------
 
-// Shapes: vectors of 16 bytes with one unit a lane, smaller ones with up to four.
-template <typename TX, typename TW, bool NORM, bool ADJ>
-RopeKernel pick_fwd(const RopeKey& k) {
-  constexpr int E = Elem<TX>::kPerVec;
-  const int id = k.e * 1000 + k.g * 10 + k.l;
-  if (id == 0) return rope_scalar_kernel<TX, TW, NORM, ADJ, false>;
-  if (id == E * 1000 + 41) return rope_kernel<TX, TW, E, 4, 1, NORM, ADJ>;
-  if (id == E * 1000 + 81) return rope_kernel<TX, TW, E, 8, 1, NORM, ADJ>;
-  if (id == E * 1000 + 161) return rope_kernel<TX, TW, E, 16, 1, NORM, ADJ>;
-  if (id == E * 1000 + 321) return rope_kernel<TX, TW, E, 32, 1, NORM, ADJ>;
-#define RMSN_ROPE(E_, G_, L_) \
-  if (id == E_ * 1000 + G_ * 10 + L_) return rope_kernel<TX, TW, E_, G_, L_, NORM, ADJ>;
-#define RMSN_ROPE_SMALL(E_) \
-  RMSN_ROPE(E_, 16, 1) RMSN_ROPE(E_, 32, 1) RMSN_ROPE(E_, 32, 2) RMSN_ROPE(E_, 32, 4)
-  RMSN_ROPE_SMALL(1) RMSN_ROPE_SMALL(2)
-  if constexpr (E == 8) { RMSN_ROPE_SMALL(4) }
-#undef RMSN_ROPE_SMALL
+// Shapes: vectors of 16 bytes with one unit a lane, smaller ones with three or
+// four, because a step of few bytes is bound by its instructions (16384 tokens x 40
+// heads, forward / backward with the norm: 36 bf16 columns in single elements, 32
+// lanes of one unit 92 / 251 us, 8 of three 64 / 101; 36 fp32 in pairs 49 / 81, 49 /
+// 62).  Vectors of four in the backward keep to two: three spill (80 bf16
+// columns 130 us, one unit 101).
+template <typename TX, typename TW, bool NORM, bool ADJ, bool BWD, int E, int G, int L, bool BLOCK>
+RopeKernel kernel_of() {
+  if constexpr (BWD) return rope_norm_bwd_kernel<TX, TW, E, G, L, ADJ, BLOCK>;
+  else return rope_kernel<TX, TW, E, G, L, NORM, ADJ, BLOCK>;
+}
+template <typename TX, typename TW, bool NORM, bool ADJ, bool BWD, int E>
+RopeKernel pick_small(int id) {
+#define RMSN_ROPE(G_, L_) \
+  if (id == G_ * 10 + L_) return kernel_of<TX, TW, NORM, ADJ, BWD, E, G_, L_, false>();
+  if constexpr (BWD && E == 4) {
+    RMSN_ROPE(4, 2) RMSN_ROPE(8, 2) RMSN_ROPE(16, 2) RMSN_ROPE(32, 2)
+  } else {
+    RMSN_ROPE(4, 3) RMSN_ROPE(4, 4) RMSN_ROPE(8, 3) RMSN_ROPE(8, 4)
+    RMSN_ROPE(16, 3) RMSN_ROPE(16, 4) RMSN_ROPE(32, 3) RMSN_ROPE(32, 4)
+  }
 #undef RMSN_ROPE
   return nullptr;
 }
-template <typename TX, typename TW, bool ADJ>
-RopeKernel pick_bwd(const RopeKey& k) {
+template <typename TX, typename TW, bool NORM, bool ADJ, bool BWD>
+RopeKernel pick_shape(const RopeKey& k) {
   constexpr int E = Elem<TX>::kPerVec;
-  const int id = k.e * 1000 + k.g * 10 + k.l;
-  if (id == 0) return rope_scalar_kernel<TX, TW, true, ADJ, true>;
-  if (id == E * 1000 + 41) return rope_norm_bwd_kernel<TX, TW, E, 4, 1, ADJ>;
-  if (id == E * 1000 + 81) return rope_norm_bwd_kernel<TX, TW, E, 8, 1, ADJ>;
-  if (id == E * 1000 + 161) return rope_norm_bwd_kernel<TX, TW, E, 16, 1, ADJ>;
-  if (id == E * 1000 + 321) return rope_norm_bwd_kernel<TX, TW, E, 32, 1, ADJ>;
-#define RMSN_ROPE(E_, G_, L_) \
-  if (id == E_ * 1000 + G_ * 10 + L_) return rope_norm_bwd_kernel<TX, TW, E_, G_, L_, ADJ>;
-#define RMSN_ROPE_SMALL(E_) \
-  RMSN_ROPE(E_, 16, 1) RMSN_ROPE(E_, 32, 1) RMSN_ROPE(E_, 32, 2) RMSN_ROPE(E_, 32, 4)
-  RMSN_ROPE_SMALL(1) RMSN_ROPE_SMALL(2)
-  if constexpr (E == 8) { RMSN_ROPE_SMALL(4) }
-#undef RMSN_ROPE_SMALL
+  if (k.e == 0) return rope_scalar_kernel<TX, TW, NORM, ADJ, BWD>;
+  if (k.e == E && k.l == 1) {
+#define RMSN_ROPE(G_) \
+  if (k.g == G_)      \
+    return k.block ? kernel_of<TX, TW, NORM, ADJ, BWD, E, G_, 1, true>() \
+                   : kernel_of<TX, TW, NORM, ADJ, BWD, E, G_, 1, false>();
+    RMSN_ROPE(4) RMSN_ROPE(8) RMSN_ROPE(16) RMSN_ROPE(32)
 #undef RMSN_ROPE
+    return nullptr;
+  }
+  if (k.block) return nullptr;
+  const int id = k.g * 10 + k.l;
+  if (k.e == 1) return pick_small<TX, TW, NORM, ADJ, BWD, 1>(id);
+  if (k.e == 2) return pick_small<TX, TW, NORM, ADJ, BWD, 2>(id);
+  if constexpr (E == 8)
+    if (k.e == 4) return pick_small<TX, TW, NORM, ADJ, BWD, 4>(id);
   return nullptr;
 }
 template <typename TX, typename TW>
 RopeKernel pick(const RopeKey& k) {
-  if (k.bwd) return k.adjacent ? pick_bwd<TX, TW, true>(k) : pick_bwd<TX, TW, false>(k);
+  if (k.bwd)
+    return k.adjacent ? pick_shape<TX, TW, true, true, true>(k)
+                      : pick_shape<TX, TW, true, false, true>(k);
   if (k.norm)
-    return k.adjacent ? pick_fwd<TX, TW, true, true>(k) : pick_fwd<TX, TW, true, false>(k);
+    return k.adjacent ? pick_shape<TX, TW, true, true, false>(k)
+                      : pick_shape<TX, TW, true, false, false>(k);
 #if RMSN_PAIR == 2   // the rotation alone has no weights: the bf16/bf16 unit has it
   return nullptr;
 #else
-  return k.adjacent ? pick_fwd<TX, TW, false, true>(k) : pick_fwd<TX, TW, false, false>(k);
+  return k.adjacent ? pick_shape<TX, TW, false, true, false>(k)
+                    : pick_shape<TX, TW, false, false, false>(k);
 #endif
 }
 
