@@ -321,7 +321,7 @@ LossKernel get_loss_sum();        // loss = sum of token_loss, one CTA
 LossKernel get_loss_pairs();      // one CTA per pair: margins, dlogp
 LossKernel get_loss_pairs_all();  // one CTA: margins, dlogp and loss
 LossKernel get_loss_pairs_mean(); // loss = mean over the pairs, one CTA
-constexpr int kLossThreads = 256;
+constexpr int kLossThreads = 256;  // at most: eight warps
 constexpr int kLossBatch = 4;     // 16-byte vectors a thread takes at a time
 constexpr int kLossStages = 3;    // batches in a thread's ring (loss with gradient)
 constexpr int kLossBwdVecs = kLossThreads * kLossBatch;   // vectors of a row per backward CTA

@@ -158,22 +158,25 @@ __device__ __forceinline__ void raise(Run& r, float m, const Scale& c) {
     r.m = m;
   }
 }
+// The warp's first N lanes merged (the others hold nothing), for all of those.
+template <int N>
 __device__ __forceinline__ Run warp_merge(Run r, const Scale& c) {
   float m;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(r.m));
   raise(r, m, c);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = N / 2; o > 0; o >>= 1) {
     const float s = __shfl_xor_sync(0xFFFFFFFFu, r.s, o), e = __shfl_xor_sync(0xFFFFFFFFu, r.e, o);
     grow(r, s, e);
   }
   r.m = m;
   return r;
 }
-// Warp 0 gets the CTA's.  part: shared, one per warp.
+// Warp 0's first eight lanes get the CTA's.  part: shared, one per warp, of which
+// there are at most eight.
 __device__ __forceinline__ Run cta_merge(Run r, const Scale& c, Run* part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  r = warp_merge(r, c);
+  r = warp_merge<32>(r, c);
   if (blockDim.x == 32) {
     __syncwarp();
     return r;
@@ -181,7 +184,7 @@ __device__ __forceinline__ Run cta_merge(Run r, const Scale& c, Run* part) {
   if (lane == 0) part[warp] = r;
   __syncthreads();
   if (warp == 0)
-    r = warp_merge(lane < (int)(blockDim.x >> 5) ? part[lane] : Run{kNegInf, 0.f, 0.f}, c);
+    r = warp_merge<8>(lane < (int)(blockDim.x >> 5) ? part[lane] : Run{kNegInf, 0.f, 0.f}, c);
   return r;
 }
 // Sum of b's terms, two at a time.
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kLossThreads, 4) loss_row_kernel(LossParams p)
     cluster_wait();
     if (tid < 32) {
       const float4 q = tid < CL ? peers[tid] : make_float4(kNegInf, 0.f, 0.f, 0.f);
-      r = warp_merge(Run{q.x, q.y, q.z}, c);
+      r = warp_merge<CL>(Run{q.x, q.y, q.z}, c);
     }
   }
   if (first && tid == 0)
@@ -693,8 +696,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) loss_stream_kernel(LossParams p
       } else {
         const float4 q =
             tid < CL ? peers[parity][tid] : make_float4(kNegInf, 0.f, 0.f, 0.f);
-        r = warp_merge(Run{q.x, q.y, q.z}, c);
-        xt = group_sum<32>(q.w);   // the others' are 0, or NaN all of them
+        r = warp_merge<CL>(Run{q.x, q.y, q.z}, c);
+        xt = group_sum<CL>(q.w);   // the others' are 0, or NaN all of them
       }
     }
     ++turn;
