@@ -2051,9 +2051,9 @@ rmsnorm_status_t launch_loss_rows(int mode, int xd, LossParams p, cudaStream_t s
   p.status = di.status;
   const int64_t nvec = p.V / per_vec(xd);
   const Force& force = read_force();
-  int cl = 1, threads, smem = 0;
+  int cl = 1, threads, stages = kLossStages, smem = 0;
   int64_t grid = 0;
-  const int64_t slots = (int64_t)di.sms * 1024;   // threads at 64 registers each
+  const int64_t slots = (int64_t)di.sms * 1024;   // threads that the SMs hold, about
   if (mode != kLossPolicyGrad) {
     // A CTA per row, small enough that a thread has some 64 vectors and CTAs at
     // other points of their rows fill the SM (fwd, bf16: 4096 x 131072 128 threads
@@ -2072,11 +2072,12 @@ rmsnorm_status_t launch_loss_rows(int mode, int xd, LossParams p, cudaStream_t s
     if (threads < 32 || threads > kLossThreads || threads % 32) return RMSNORM_ERR_INVALID_ARG;
     grid = p.M * cl;
   } else {
-    // CTAs that hold three quarters or more of their part of a row in their ring
-    // (12 of 16 vectors a thread): one CTA of up to 256 threads, or a cluster of
-    // CTAs of 128 (4096 x 131072 bf16: eight of 128 threads 363 us, four of 256 376,
-    // two of 512 377; 8192 x 32768: one of 256 184, two of 128 196).  Few rows: more
-    // CTAs a row.
+    // CTAs that hold their part of a row in their ring (16 vectors a thread): one
+    // CTA of up to 256 threads, or a cluster of CTAs of 128 (4096 x 131072 bf16: eight of
+    // 128 threads 349 us, four of 256 359; 8192 x 32768: one of 256 176, two of 128
+    // 190).  Few rows: more CTAs a row.  CTAs of a warp take a ring of two batches
+    // instead of four, so that 28 of them fit an SM (32768 x 2000 bf16: 52 us, with
+    // three batches 58, with four 69).
     threads = 32;
     while (threads < 256 && nvec > 16 * threads) threads *= 2;
     if (nvec > 16 * 256 && nvec <= 8 * 16 * 128) threads = 128;
@@ -2086,10 +2087,11 @@ rmsnorm_status_t launch_loss_rows(int mode, int xd, LossParams p, cudaStream_t s
       cl *= 2;
     if (force.on && force.cl) cl = force.cl;
     if (force.on && force.threads) threads = force.threads;
-    smem = kLossStages * kLossBatch * 16 * threads;
+    stages = loss_stages(threads);
+    smem = stages * kLossBatch * 16 * threads;
   }
-  const LossKernel fn =
-      xd == kF32 ? get_loss_rows_f32(mode, cl, threads) : get_loss_rows_bf16(mode, cl, threads);
+  const LossKernel fn = xd == kF32 ? get_loss_rows_f32(mode, cl, threads, stages)
+                                   : get_loss_rows_bf16(mode, cl, threads, stages);
   if (!fn) return RMSNORM_ERR_INVALID_ARG;
   if (grid == 0) {   // persistent: the clusters that the device holds at once
     const void* f = reinterpret_cast<const void*>(fn);

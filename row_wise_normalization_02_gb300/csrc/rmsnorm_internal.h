@@ -312,9 +312,9 @@ struct LossParams {
 enum LossMode : int { kLossLogprob = 0, kLossPolicy = 1, kLossPolicyGrad = 2, kLossPreference = 3 };
 using LossKernel = void (*)(LossParams);
 // Kernel of a mode for clusters of `cluster` CTAs per row (with the gradient: for
-// CTAs of `threads` threads).
-LossKernel get_loss_rows_f32(int mode, int cluster, int threads);
-LossKernel get_loss_rows_bf16(int mode, int cluster, int threads);
+// CTAs of `threads` threads with rings of `stages` batches).
+LossKernel get_loss_rows_f32(int mode, int cluster, int threads, int stages);
+LossKernel get_loss_rows_bf16(int mode, int cluster, int threads, int stages);
 LossKernel get_loss_bwd_f32();
 LossKernel get_loss_bwd_bf16();
 LossKernel get_loss_sum();        // loss = sum of token_loss, one CTA
@@ -323,7 +323,8 @@ LossKernel get_loss_pairs_all();  // one CTA: margins, dlogp and loss
 LossKernel get_loss_pairs_mean(); // loss = mean over the pairs, one CTA
 constexpr int kLossThreads = 256;  // at most: eight warps
 constexpr int kLossBatch = 4;     // 16-byte vectors a thread takes at a time
-constexpr int kLossStages = 3;    // batches in a thread's ring (loss with gradient)
+constexpr int kLossStages = 4;    // batches in a thread's ring (loss with gradient)
+constexpr int loss_stages(int threads) { return threads == 32 ? 2 : kLossStages; }
 constexpr int kLossBwdVecs = kLossThreads * kLossBatch;   // vectors of a row per backward CTA
 
 // Threads per CTA of the subwarp families; upper bound of the per-row CTAs.

@@ -506,22 +506,25 @@ __device__ __forceinline__ void copy_wait() {
 // for its own copies only.
 //
 // A row is gone over twice, the second time backwards: its last S batches are
-// still in the ring, and only what lies before them is fetched again -- from L2,
-// where it was a moment ago.  Batch i of a row lies in stage base + i, or base - i
-// in every other row: the second pass frees the stages in the opposite order, and
-// the next row's batches fill them so.  Each step of either pass commits one
-// group (an empty one where there is nothing to fetch), so the data a step needs
-// is always the S-th last group.
+// still in the ring -- all of them, where a CTA's part is no longer -- and only what
+// lies before them is fetched again, from L2, where it was a moment ago.  Batch i
+// of a row lies in stage base + i, or base - i in every other row: the second pass
+// frees the stages in the opposite order, and the next row's batches fill them so.
+// Each step of either pass commits one group (an empty one where there is nothing
+// to fetch), so the data a step needs is always the S-th last group.
 //
-// 1024 threads an SM in CTAs as small as a row's part allows: an SM can store 32
-// bytes a clock, so a row of 256 KB takes 4.4 us to write wherever it is written
-// from, and the only way to keep loads, sums and stores all going is to have
-// several rows at different points on every SM.  A row split over a cluster keeps
-// the rows under way -- and the L2 they need -- few.
-template <typename TX, int NT, int CL>
-__global__ void __launch_bounds__(NT, 1024 / NT) loss_stream_kernel(LossParams p) {
+// What bounds it.  DRAM would take 285 us for 4096 x 131072 bf16 with a fifth of the
+// rows left out; this takes 349 (5.5 TB/s).  A CTA's passes are short, and its
+// merges, the exchange with its peers and the loss between them -- some 8000 of a
+// row's 25000 clocks -- leave its warps idle, so an SM needs many CTAs at different
+// points: 896 threads of it in CTAs as small as a row's part allows, the 64 bytes of
+// ring for a thread and batch being what 227 KB hold.  (One CTA of 1024 threads per
+// SM with the same ring 377 us; three quarters of a row in the ring 362.)  An SM
+// stores at most 32 bytes a clock, from wherever: 4.4 us for a row of 256 KB.
+template <typename TX, int NT, int CL, int S>
+__global__ void __launch_bounds__(NT, 896 / NT) loss_stream_kernel(LossParams p) {
   constexpr int MODE = kLossPolicyGrad;
-  constexpr int E = Elem<TX>::kPerVec, U = kLossBatch, S = kLossStages;
+  constexpr int E = Elem<TX>::kPerVec, U = kLossBatch;
   extern __shared__ uint4 ring[];   // [S][U][NT]
   __shared__ Run part[2][32];
   __shared__ float4 peers[2][8];   // m, s, e and, from the CTA that has it, the target's logit
@@ -1011,27 +1014,28 @@ LossKernel pick_row(int cluster) {
   }
 }
 template <typename TX>
-LossKernel pick_stream(int cluster, int threads) {
+LossKernel pick_stream(int cluster, int threads, int stages) {
+  if (stages != loss_stages(threads)) return nullptr;
   switch (cluster * 1000 + threads) {
-    case 1032: return loss_stream_kernel<TX, 32, 1>;
-    case 1064: return loss_stream_kernel<TX, 64, 1>;
-    case 1128: return loss_stream_kernel<TX, 128, 1>;
-    case 1256: return loss_stream_kernel<TX, 256, 1>;
-    case 2128: return loss_stream_kernel<TX, 128, 2>;
-    case 4128: return loss_stream_kernel<TX, 128, 4>;
-    case 8128: return loss_stream_kernel<TX, 128, 8>;
-    case 2256: return loss_stream_kernel<TX, 256, 2>;
-    case 4256: return loss_stream_kernel<TX, 256, 4>;
-    case 8256: return loss_stream_kernel<TX, 256, 8>;
+    case 1032: return loss_stream_kernel<TX, 32, 1, loss_stages(32)>;
+    case 1064: return loss_stream_kernel<TX, 64, 1, kLossStages>;
+    case 1128: return loss_stream_kernel<TX, 128, 1, kLossStages>;
+    case 1256: return loss_stream_kernel<TX, 256, 1, kLossStages>;
+    case 2128: return loss_stream_kernel<TX, 128, 2, kLossStages>;
+    case 4128: return loss_stream_kernel<TX, 128, 4, kLossStages>;
+    case 8128: return loss_stream_kernel<TX, 128, 8, kLossStages>;
+    case 2256: return loss_stream_kernel<TX, 256, 2, kLossStages>;
+    case 4256: return loss_stream_kernel<TX, 256, 4, kLossStages>;
+    case 8256: return loss_stream_kernel<TX, 256, 8, kLossStages>;
     default: return nullptr;
   }
 }
 template <typename TX>
-LossKernel pick_mode(int mode, int cluster, int threads) {
+LossKernel pick_mode(int mode, int cluster, int threads, int stages) {
   switch (mode) {
     case kLossLogprob: return pick_row<TX, kLossLogprob>(cluster);
     case kLossPolicy: return pick_row<TX, kLossPolicy>(cluster);
-    case kLossPolicyGrad: return pick_stream<TX>(cluster, threads);
+    case kLossPolicyGrad: return pick_stream<TX>(cluster, threads, stages);
     case kLossPreference: return pick_row<TX, kLossPreference>(cluster);
     default: return nullptr;
   }
@@ -1040,8 +1044,8 @@ LossKernel pick_mode(int mode, int cluster, int threads) {
 }  // namespace
 
 #if RMSN_PAIR == 0
-LossKernel get_loss_rows_f32(int mode, int cluster, int threads) {
-  return pick_mode<float>(mode, cluster, threads);
+LossKernel get_loss_rows_f32(int mode, int cluster, int threads, int stages) {
+  return pick_mode<float>(mode, cluster, threads, stages);
 }
 LossKernel get_loss_bwd_f32() { return loss_bwd_kernel<float>; }
 LossKernel get_loss_sum() { return loss_sum_kernel; }
@@ -1049,8 +1053,8 @@ LossKernel get_loss_pairs() { return loss_pairs_kernel; }
 LossKernel get_loss_pairs_all() { return loss_pairs_all_kernel; }
 LossKernel get_loss_pairs_mean() { return loss_pairs_mean_kernel; }
 #else
-LossKernel get_loss_rows_bf16(int mode, int cluster, int threads) {
-  return pick_mode<bf16>(mode, cluster, threads);
+LossKernel get_loss_rows_bf16(int mode, int cluster, int threads, int stages) {
+  return pick_mode<bf16>(mode, cluster, threads, stages);
 }
 LossKernel get_loss_bwd_bf16() { return loss_bwd_kernel<bf16>; }
 #endif
