@@ -303,7 +303,8 @@ rmsnorm_status_t rmsnorm_check_device(cudaStream_t stream);
  *
  * A [T, H, D] view: element (t, h, d) at data[t * stride_token + h *
  * stride_head + d].  Strides are in elements, non-negative, and the rows of a
- * view must not overlap (as in rmsnorm_fwd_strided).
+ * view must not overlap: either a token's heads lie within one stride_token, or a
+ * head's tokens within one stride_head (heads first).
  */
 typedef struct rmsnorm_heads {
   void* data;            /* device pointer */
@@ -339,7 +340,7 @@ typedef enum rmsnorm_rope_order {
  */
 typedef struct rmsnorm_rope {
   const int64_t* positions;  /* [axes, T] */
-  int64_t positions_stride;  /* elements from one axis to the next, >= T when axes > 1 */
+  int64_t positions_stride;  /* elements from one axis to the next, T .. 2^56 when axes > 1 */
   const float* inv_freq;     /* [R / 2] */
   int64_t rotary_dim;        /* R: even, 2 <= R <= D */
   int32_t axes;              /* 1 .. RMSNORM_ROPE_MAX_AXES */
@@ -360,7 +361,7 @@ typedef struct rmsnorm_rope {
  * otherwise no output shares memory with another operand.  Views cut side by
  * side out of one buffer are apart: q and k of a fused projection's rows (equal
  * token strides), or heads in turn (equal head strides that divide the token
- * strides).  D <= RMSNORM_ROPE_MAX_D,
+ * strides, or equal token strides that divide the head strides).  D <= RMSNORM_ROPE_MAX_D,
  * T < 2^30, Hq + Hk <= 2^16.  The kernels work in vectors of 16 bytes where
  * starts and strides are multiples of that and D and R of two of them, of 8, 4
  * or 2 bytes otherwise; rows beyond 64 vectors of 16 bytes or 256 smaller ones
@@ -488,7 +489,7 @@ rmsnorm_status_t rmsnorm_policy_loss_fwd(const void* logits, int64_t ld, const i
  * and dlogp_i the derivative of loss by logp_i (0 in rows of no sequence).
  * ref_logp: M fp32 per token, or NULL for 0.  cu_seqlens: 2 * pairs + 1 int64
  * on the device, not decreasing, within [0, M] (offsets outside are cut to the
- * batch); an empty sequence has S = 0.  S and the margins are summed in 64 bits.
+ * batch); an empty sequence has S = 0.  Sums are held in two fp32 parts (some 45 bits).
  * 1 <= pairs < 2^24, beta finite, 0 <= label_smoothing <= 1.  loss: one fp32;
  * margins: `pairs` fp32; logp, rel_lse, dlogp: M fp32 each.  The gradient of the
  * logits comes from rmsnorm_token_logprob_bwd.

@@ -178,12 +178,13 @@ class _LayerNorm(torch.autograd.Function):
 
 def _rows_of_heads(t: torch.Tensor) -> torch.Tensor:
     """t as [T, H, D] in a layout the kernels address: contiguous rows that do not
-    overlap; copied where it is not."""
+    overlap (a token's heads side by side, or a head's tokens); copied where it is not."""
     t = t.flatten(0, -3)
     T, H, D = t.shape
     st, sh, sd = t.stride()
-    ok = (sd == 1 or D == 1) and (H < 2 or sh >= D) and (T < 2 or st >= (H - 1) * sh + D)
-    return t if ok else t.contiguous()
+    tokens_apart = (H < 2 or sh >= D) and (T < 2 or st >= (H - 1) * sh + D)
+    heads_apart = (T < 2 or st >= D) and (H < 2 or sh >= (T - 1) * st + D)
+    return t if (sd == 1 or D == 1) and (tokens_apart or heads_apart) else t.contiguous()
 
 
 class _Rope(torch.autograd.Function):
@@ -248,7 +249,7 @@ def _apply_rope(q, k, q_gamma, k_gamma, positions, inv_freq, sections, pairs, or
     for w in (q_gamma, k_gamma):
         if w is not None and (w.shape != (D,) or not w.is_contiguous()):
             raise ValueError(f"weights must be contiguous vectors of {D}")
-    if k_gamma is not None and k_gamma.dtype != q_gamma.dtype:
+    if k_gamma is not None and (q_gamma is None or k_gamma.dtype != q_gamma.dtype):
         raise ValueError("q_gamma and k_gamma must have the same dtype")
     sections = tuple(int(n) for n in sections)
     rotary_dim = 2 * sum(sections)
@@ -296,10 +297,11 @@ def _row_stride(rows):
 
 
 def _gradient_rows(rows):
-    """An empty [M, V] with the rows' stride and their starts modulo 16 bytes, so that
-    reads and writes fall on the same vectors."""
+    """An empty [M, V] whose rows start where those of `rows` do modulo 16 bytes, so
+    that reads and writes fall on the same vectors."""
     M, V = rows.shape
-    ld = _row_stride(rows)
+    per = 16 // rows.element_size()
+    ld = V + (_row_stride(rows) - V) % per
     off = rows.data_ptr() % 16 // rows.element_size()
     flat = torch.empty(off + max(M * ld, 1), dtype=rows.dtype, device=rows.device)
     return flat[off:].as_strided((M, V), (ld, 1), off)
@@ -415,6 +417,8 @@ def rms_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_gamma: torch.Tensor
                   sections, pairs: str = "halves", order: str = "blocks", eps: float = 1e-6):
     """rope(rms_norm(q, q_gamma), rms_norm(k, k_gamma)) over each head's D elements, in one
     pass and one rounding."""
+    if q_gamma is None:
+        raise ValueError("q_gamma is wanted: rope() is the rotation alone")
     return _apply_rope(q, k, q_gamma, k_gamma, positions, inv_freq, sections, pairs, order, eps)
 
 

@@ -1629,7 +1629,9 @@ rmsnorm_status_t check_rope(const rmsnorm_rope_t* r, int64_t T, int64_t D) {
       return RMSNORM_ERR_INVALID_ARG;
     sum += n;
   }
-  if (sum != half || (r->axes > 1 && r->positions_stride < T)) return RMSNORM_ERR_INVALID_ARG;
+  if (sum != half || (r->axes > 1 && (r->positions_stride < T ||
+                                      r->positions_stride > (int64_t(1) << 56))))
+    return RMSNORM_ERR_INVALID_ARG;
   if (T == 0) return RMSNORM_OK;
   if (!r->positions || !r->inv_freq) return RMSNORM_ERR_INVALID_ARG;
   if (!aligned_to(r->positions, 8) || !aligned_to(r->inv_freq, 4)) return RMSNORM_ERR_MISALIGNED;
@@ -1640,15 +1642,18 @@ rmsnorm_status_t check_rope(const rmsnorm_rope_t* r, int64_t T, int64_t D) {
 // 63 bits.
 bool view_span(const rmsnorm_heads_t& v, int64_t T, int64_t D, int es, size_t* bytes) {
   *bytes = 0;
-  if (!strided_layout_ok(1, v.heads, D, v.stride_token, v.stride_head)) return false;
+  const int64_t st = v.stride_token, sh = v.stride_head, limit = int64_t(1) << 59;
+  if (st < 0 || sh < 0) return false;
   if (T == 0 || v.heads == 0) return true;
   int64_t a, b;
-  if (__builtin_mul_overflow(T - 1, v.stride_token, &a) ||
-      __builtin_mul_overflow(v.heads - 1, v.stride_head, &b) || b > (int64_t(1) << 60) ||
-      (T > 1 && v.stride_token < b + D) || __builtin_add_overflow(a, b + D, &a) ||
-      a > (int64_t(1) << 60))
+  if (__builtin_mul_overflow(T - 1, st, &a) || __builtin_mul_overflow(v.heads - 1, sh, &b) ||
+      a > limit || b > limit)
     return false;
-  *bytes = (size_t)a * (size_t)es;
+  // a token's heads side by side, or a head's tokens
+  const bool tokens_apart = (v.heads == 1 || sh >= D) && (T == 1 || st >= b + D);
+  const bool heads_apart = (T == 1 || st >= D) && (v.heads == 1 || sh >= a + D);
+  if (!tokens_apart && !heads_apart) return false;
+  *bytes = (size_t)(a + b + D) * (size_t)es;
   return true;
 }
 
@@ -1663,8 +1668,8 @@ struct Span {
 // Whether two operands may share a byte.  Views cut out of one buffer side by
 // side (q and k of a fused projection's rows; k and v heads in turn) cover each
 // other's range without sharing a row: with equal token strides their tokens'
-// row ranges, or with equal head strides that divide the token strides their
-// rows, are compared modulo that stride.
+// row ranges, or with equal head strides that divide the token strides (or the
+// other way round) their rows, are compared modulo that stride.
 bool spans_overlap(const Span& a, const Span& b, int64_t D, int es) {
   if (!overlap(a.p, a.n, b.p, b.n)) return false;
   if (!a.view || !b.view) return true;
@@ -1676,15 +1681,16 @@ bool spans_overlap(const Span& a, const Span& b, int64_t D, int es) {
     const int64_t m = ((d % period) + period) % period;
     return m >= wu && m + wv <= period;
   };
+  auto rows_apart = [&](int64_t su, int64_t sv, int64_t other_u, int64_t other_v) {
+    return su == sv && su > 0 && other_u % su == 0 && other_v % su == 0 &&
+           apart(su * es, D * es, D * es);
+  };
   if (u.stride_token == v.stride_token &&
       apart(u.stride_token * es, ((u.heads - 1) * u.stride_head + D) * es,
             ((v.heads - 1) * v.stride_head + D) * es))
     return false;
-  if (u.stride_head == v.stride_head && u.stride_head > 0 &&
-      u.stride_token % u.stride_head == 0 && v.stride_token % u.stride_head == 0 &&
-      apart(u.stride_head * es, D * es, D * es))
-    return false;
-  return true;
+  return !rows_apart(u.stride_head, v.stride_head, u.stride_token, v.stride_token) &&
+         !rows_apart(u.stride_token, v.stride_token, u.stride_head, v.stride_head);
 }
 
 // Largest power of two, at most 16, that a view's start and strides are multiples
@@ -1780,7 +1786,11 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
   int ns = 0;   // at most 3 views, gamma and dgamma per side, 2 of the rotation, the workspace
   int align = 16;
   for (int i = 0; i < 2; ++i) {
-    if (heads[i] == 0) continue;
+    if (dgamma[i] && !aligned_to(dgamma[i], 4)) return RMSNORM_ERR_MISALIGNED;
+    if (heads[i] == 0) {
+      if (dgamma[i]) spans[ns++] = Span{dgamma[i], (size_t)D * 4, true, nullptr};
+      continue;
+    }
     const rmsnorm_heads_t* views[3] = {!bwd || norm ? x[i] : nullptr, bwd ? dy[i] : nullptr,
                                        out[i]};
     const bool need[3] = {!bwd || norm, bwd, true};
@@ -1803,9 +1813,7 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
       else spans[ns - 1].written = true;   // `from` is the view added just before
     }
     if (norm) {
-      if (!aligned_to(gamma[i], (size_t)esize(wd)) ||
-          (dgamma[i] && !aligned_to(dgamma[i], 4)))
-        return RMSNORM_ERR_MISALIGNED;
+      if (!aligned_to(gamma[i], (size_t)esize(wd))) return RMSNORM_ERR_MISALIGNED;
       if (align == 16 && !aligned_to(gamma[i], 16)) align = 8;   // 16-byte vectors of it too
       spans[ns++] = Span{gamma[i], (size_t)D * esize(wd), false, nullptr};
       if (dgamma[i]) spans[ns++] = Span{dgamma[i], (size_t)D * 4, true, nullptr};
@@ -1953,7 +1961,7 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
 // ---------------------------------------------------------------- token losses
 
 constexpr int64_t kLossMaxM = (int64_t(1) << 28) - 1;
-constexpr int64_t kLossOneCta = 32768;
+constexpr int64_t kLossOneCta = 4096;
 
 // Operands of a loss call, checked for NULL, alignment and overlap as they are
 // listed.
@@ -2050,7 +2058,8 @@ rmsnorm_status_t launch_loss_rows(int mode, int xd, LossParams p, cudaStream_t s
   p.wait_limit = wait_limit();
   p.status = di.status;
   const int64_t nvec = p.V / per_vec(xd);
-  const Force& force = read_force();
+  // ("loss:cl=4:t=128"; a form that names another family is not meant for these)
+  const Force force = read_force().family < 0 ? read_force() : Force();
   int cl = 1, threads, stages = kLossStages, smem = 0;
   int64_t grid = 0;
   const int64_t slots = (int64_t)di.sms * 1024;   // threads that the SMs hold, about
@@ -2248,8 +2257,9 @@ rmsnorm_status_t preference_loss_impl(const void* logits, int64_t ld, const int6
   p.margins = margins;
   p.loss = loss;
   if (M > 0 && (st = launch_loss_rows(kLossPreference, xd, p, stream)) != RMSNORM_OK) return st;
-  // one CTA for all of it up to kLossOneCta rows (8192 rows: 4 us against 3 + 2 in two
-  // launches), else a CTA per pair and one for the mean
+  // One CTA for all of it up to kLossOneCta rows, else a CTA per pair and one for the
+  // mean.  On the GPU two launches are ahead (256 rows in 4 pairs: 4.2 us against 5.0,
+  // 2048 in 8: 3.9 / 5.3, 8192 in 16: 4.3 / 7.6), but one more costs the host 2 us.
   const bool one = M <= kLossOneCta;
   if ((st = launch_loss(one ? get_loss_pairs_all() : get_loss_pairs(), one ? 1 : pairs,
                         one ? 1024 : kLossThreads, p, stream, "preference margins launch")) !=
@@ -2655,8 +2665,8 @@ rmsnorm_status_t rmsnorm_preference_loss_fwd(const void* logits, int64_t ld,
                                              const int64_t* targets, double inv_temperature,
                                              const float* ref_logp, const int64_t* cu_seqlens,
                                              int64_t pairs, float beta, float label_smoothing,
-                                             float* loss, float* margins, float* logp, float* rel_lse,
-                                             float* dlogp, int64_t M, int64_t V,
+                                             float* loss, float* margins, float* logp,
+                                             float* rel_lse, float* dlogp, int64_t M, int64_t V,
                                              rmsnorm_dtype_t x_dtype, cudaStream_t stream) {
   return preference_loss_impl(logits, ld, targets, inv_temperature, ref_logp, cu_seqlens, pairs,
                               beta, label_smoothing, loss, margins, logp, rel_lse, dlogp, M, V,

@@ -25,6 +25,7 @@
 
 #include "rmsnorm_device.cuh"
 #include "rmsnorm_internal.h"
+#include "rmsnorm_ring.cuh"   // kDrainLimit
 
 #ifndef RMSN_PAIR
 #error "compile once per dtype with -DRMSN_PAIR=0 (f32), 1 (bf16)"
@@ -73,12 +74,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 
 // x - o of a vector's elements in pairs; bf16 ones straight from the packed halves
 // by the mixed-precision fma (x 1 - o), which saves unpacking them.
-[[maybe_unused]] __device__ __forceinline__ void differences(const uint4& v, float o, float2 (&d)[2]) {
+[[maybe_unused]] __device__ __forceinline__ void differences(const uint4& v, float o,
+                                                             float2 (&d)[2]) {
   const float2 n = make_float2(-o, -o);
   d[0] = add2(make_float2(__uint_as_float(v.x), __uint_as_float(v.y)), n);
   d[1] = add2(make_float2(__uint_as_float(v.z), __uint_as_float(v.w)), n);
 }
-[[maybe_unused]] __device__ __forceinline__ void differences(const uint4& v, float o, float2 (&d)[4]) {
+[[maybe_unused]] __device__ __forceinline__ void differences(const uint4& v, float o,
+                                                             float2 (&d)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -275,9 +278,9 @@ __device__ __forceinline__ Frame frame_of(const TX* row, int V) {
 
 // ---------------------------------------------------------------- per-row losses
 
-// A value in two fp32 parts, some 45 bits, on the fp32 pipe: a row's few 64-bit
-// operations kept the fp64 pipe, at two lanes a clock, busy for 200 clocks, which
-// bounded short rows.  The low part of a value that is not finite is 0.
+// A value in two fp32 parts, some 45 bits, on the fp32 pipe: the fp64 pipe has two
+// lanes a clock for all of an SM's rows, which bounds short ones.  The low part of a
+// value that is not finite is 0.
 struct Two {
   float hi, lo;
 };
@@ -692,6 +695,8 @@ __global__ void __launch_bounds__(NT, 896 / NT) loss_stream_kernel(LossParams p)
       }
       const bool ok = mbar_wait_bounded(bar + parity, (turn >> 1) & 1, p.wait_limit);
       if (__any_sync(0xFFFFFFFFu, !ok)) {
+        // (the peers' pushes of this row land before the CTA leaves)
+        mbar_wait_bounded(bar + parity, (turn >> 1) & 1, kDrainLimit);
         if (tid == 0) {
           atomicOr(p.status, kStatusWaitTimeout);
           stop = 1;
@@ -859,8 +864,8 @@ __global__ void __launch_bounds__(kLossThreads, 4) loss_bwd_kernel(LossParams p)
 constexpr int kSumThreads = 1024;
 
 // A sum in two fp32 parts: each addition's rounding error is exact and goes to
-// the low part, so the sum has some 45 bits -- on the fp32 pipe (the fp64 one
-// took 18 us for the 4096 rows that this takes 2 us for).
+// the low part, so the sum has some 45 bits -- on the fp32 pipe (in fp64 it made a
+// policy loss over 4096 rows 16 us longer).
 struct Sum2 {
   float hi, lo;
 };
@@ -873,26 +878,35 @@ __device__ __forceinline__ void add(Sum2& s, float x, float low = 0.f) {
 }
 __device__ __forceinline__ float value_of(const Sum2& s) { return s.hi + s.lo; }
 
-// Sum over the CTA in a fixed order; every thread gets it.
-__device__ __forceinline__ Sum2 cta_sum2(Sum2 v, float2* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+// Sum over groups of `n` lanes (a power of two) in a fixed order; all of them get it.
+__device__ __forceinline__ Sum2 lanes_sum2(Sum2 v, int n) {
+  for (int o = n / 2; o > 0; o >>= 1) {
     const float hi = __shfl_xor_sync(0xFFFFFFFFu, v.hi, o);
     const float lo = __shfl_xor_sync(0xFFFFFFFFu, v.lo, o);
     add(v, hi, lo);
   }
+  return v;
+}
+// Sum over groups of `warps` warps (a power of two) in a fixed order; every thread
+// gets its group's.
+__device__ __forceinline__ Sum2 warps_sum2(Sum2 v, float2* red, int warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = lanes_sum2(v, 32);
   __syncthreads();   // earlier readers of red are done
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(v.hi, v.lo);
+  if (lane == 0) red[warp] = make_float2(v.hi, v.lo);
   __syncthreads();
-  Sum2 s{0.f, 0.f};
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) add(s, red[w].x, red[w].y);
-  return s;
+  const float2 q = red[(warp & -warps) + (lane & (warps - 1))];
+  return lanes_sum2(Sum2{q.x, q.y}, warps);
+}
+__device__ __forceinline__ Sum2 cta_sum2(Sum2 v, float2* red) {
+  return warps_sum2(v, red, blockDim.x >> 5);
 }
 
 __global__ void __launch_bounds__(kSumThreads) loss_sum_kernel(LossParams p) {
   __shared__ float2 red[32];
   pdl_begin();
   Sum2 s{0.f, 0.f};
+#pragma unroll 4
   for (int64_t i = threadIdx.x; i < p.M; i += kSumThreads) add(s, p.token_loss[i]);
   s = cta_sum2(s, red);
   if (threadIdx.x == 0) *p.loss = value_of(s);
@@ -929,6 +943,7 @@ __device__ __forceinline__ PairRows pair_rows(const LossParams& p, int64_t b) {
 __device__ __forceinline__ Sum2 pair_sum(const LossParams& p, const PairRows& r, int i, int n) {
   Sum2 sum{0.f, 0.f};
   for (int side = 0; side < 2; ++side)
+#pragma unroll 4
     for (int64_t k = r.a[side] + i; k < r.e[side]; k += n)
       add(sum, side ? -p.dlogp[k] : p.dlogp[k]);
   return sum;
@@ -939,6 +954,7 @@ __device__ __forceinline__ void pair_slopes(const LossParams& p, const PairRows&
   const float slope = (p.smoothing / (1.f + expf(-h)) - (1.f - p.smoothing) / (1.f + expf(h))) *
                       (p.beta / (float)p.pairs);
   for (int side = 0; side < 2; ++side)
+#pragma unroll 4
     for (int64_t k = r.a[side] + i; k < r.e[side]; k += n)
       p.dlogp[k] = p.targets[k] < 0 ? 0.f : side ? -slope : slope;
 }
@@ -969,27 +985,14 @@ __global__ void __launch_bounds__(kSumThreads) loss_pairs_all_kernel(LossParams 
   pdl_begin();
   int group = W;   // warps per pair
   while (group > 1 && W / group < p.pairs) group /= 2;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int i = threadIdx.x % (32 * group), n = 32 * group;
   Sum2 losses{0.f, 0.f};
   for (int64_t b0 = 0; b0 < p.pairs; b0 += W / group) {
     const int64_t b = b0 + warp / group;
     PairRows r{};
     if (b < p.pairs) r = pair_rows(p, b);
-    Sum2 s = pair_sum(p, r, i, n);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float hi = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o);
-      const float lo = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
-      add(s, hi, lo);
-    }
-    __syncthreads();   // the previous pairs' sums have been read
-    if (lane == 0) red[warp] = make_float2(s.hi, s.lo);
-    __syncthreads();
-    s = Sum2{0.f, 0.f};
-    for (int w = warp / group * group; w < (warp / group + 1) * group; ++w)
-      add(s, red[w].x, red[w].y);
-    const float h = p.beta * value_of(s);
+    const float h = p.beta * value_of(warps_sum2(pair_sum(p, r, i, n), red, group));
     if (b < p.pairs) {
       pair_slopes(p, r, h, i, n);
       if (i == 0) {

@@ -21,13 +21,15 @@
 //
 // What bounds it: memory.  Every element is read once and written once (the
 // backward with the norm reads x and dy), against about 4-10 fp32 instructions
-// per element.  A warp takes one token (or a chunk of its heads where tokens
-// are few): its lanes compute the token's R / 2 sines and cosines once into
-// the warp's shared memory, each lane takes the ones of its columns into
+// per element.  A warp takes one token (a chunk of its heads where tokens are few, a
+// block of tokens where heads are): its lanes compute the R / 2 sines and cosines
+// once into the warp's shared memory, each lane takes the ones of its columns into
 // registers, and the warp then walks the heads, 32 / G rows at a time.  A lane
-// holds two 16-byte vectors of a row, chosen so that both halves of every pair
-// are its own (columns i.. and R/2 + i.. for halves, neighbours for adjacent
-// pairs): the rotation needs no exchange.
+// holds L units of two vectors of a row, chosen so that both columns of every pair
+// are its own (vectors of either half for halves, within a vector for adjacent
+// pairs): the rotation needs no exchange.  Rows arrive by cp.async in a ring of
+// which every thread reads back only what it copied itself, so that loads stay in
+// flight through the arithmetic and no barrier waits for them.
 #include "rmsnorm_device.cuh"
 #include "rmsnorm_internal.h"
 
@@ -92,8 +94,12 @@ template <> struct Raw<8> { uint2 v; };
 template <> struct Raw<4> { uint32_t v; };
 template <> struct Raw<2> { uint16_t v; };
 
-[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<16>& r, float (&f)[4]) { unpack(r.v, f); }
-[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<16>& r, float (&f)[8]) { unpack(r.v, f); }
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<16>& r, float (&f)[4]) {
+  unpack(r.v, f);
+}
+[[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<16>& r, float (&f)[8]) {
+  unpack(r.v, f);
+}
 [[maybe_unused]] __device__ __forceinline__ void unpack_raw(const Raw<8>& r, float (&f)[2]) {
   f[0] = __uint_as_float(r.v.x);
   f[1] = __uint_as_float(r.v.y);
@@ -203,7 +209,9 @@ __device__ __forceinline__ void unit_vectors(const RopeParams& p, int u, int* a,
 }
 
 // Operations on pairs of registers, E / 2 at a time (E = 1: one).
-__device__ __forceinline__ float2 pair_at(const float* a, int i) { return make_float2(a[i], a[i + 1]); }
+__device__ __forceinline__ float2 pair_at(const float* a, int i) {
+  return make_float2(a[i], a[i + 1]);
+}
 __device__ __forceinline__ void put_pair(float* a, int i, float2 v) {
   a[i] = v.x;
   a[i + 1] = v.y;
@@ -717,8 +725,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
 }
 
 // ---------------------------------------------------------------------------
-// Scalar form of both, for rows or columns that do not fall on 16-byte vectors
-// and for more than 64 of them: a CTA per (token, chunk), the angles in shared
+// Scalar form of both, for rows that reach further than the vectors of their
+// alignment do: a CTA per (token, chunk), the angles in shared
 // memory, each thread the pairs i = tid, tid + threads, ... and, behind them,
 // the unrotated columns.
 template <typename TX, typename TW, bool NORM, bool ADJ, bool BWD>

@@ -123,6 +123,12 @@ class Case:
             if layout == "turns":        # q and k heads in turn (hq == hk)
                 b = block(2 * heads_q).view(T, heads_q, 2, D)
                 return b[:, :, 0], b[:, :, 1], b
+            if layout == "heads":        # [H, T, D]
+                return (block(heads_q).view(heads_q, T, D).transpose(0, 1),
+                        block(heads_k).view(heads_k, T, D).transpose(0, 1), None)
+            if layout == "heads, in turn":   # [H, T, q and k, D] (hq == hk)
+                b = block(2 * heads_q).view(heads_q, T, 2, D).transpose(0, 1)
+                return b[:, :, 0], b[:, :, 1], b
             return block(heads_q), block(heads_k), None
 
         self.q, self.k, self.base = two(hq, hk)
@@ -233,7 +239,7 @@ def test_far_and_negative_positions(far):
 
 
 @gpu
-@pytest.mark.parametrize("layout", ["packed", "apart", "turns"])
+@pytest.mark.parametrize("layout", ["packed", "apart", "turns", "heads", "heads, in turn"])
 @pytest.mark.parametrize("offset", [0, 1, 8])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_layouts(layout, offset, in_place):
@@ -305,6 +311,24 @@ def test_no_rows():
 
 
 @gpu
+def test_a_view_of_no_heads_has_a_zero_gradient():
+    for D in (64, 2050):      # the vectors' kernel and the scalar one
+        c = Case(5, 3, 2, D, D, [D // 2], layout="apart")
+        none = rn.Heads(None, 0, 0, 0)
+        gq, gk = torch.full((2, D), float("nan"), device="cuda")
+        n = rn.rmsnorm_rope_bwd_workspace_size(5, 3, 0, D, "bf16", "bf16")
+        ws, dq = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(c.dyq)
+        rn.rmsnorm_rope_bwd(rn.Heads.of(c.dyq), none, rn.Heads.of(c.q), none, c.gq, c.gk,
+                            rn.Heads.of(dq), none, gq, gk, ws, n, c.rope, 5, D, c.eps, "bf16",
+                            "bf16")
+        dx, tol, dg, dgtol = ref_bwd(c.host(c.dyq), c.host(c.q), c.host(c.gq), c.eps, c.cos, c.sin,
+                                     D, "halves")
+        check(dq, dx, tol, "bf16")
+        check(gq, dg, dgtol)
+        assert not gk.any()
+
+
+@gpu
 def test_special_values_stay_in_their_row():
     c = Case(6, 4, 1, 64, 64, [32], xd="f32")
     clean = [t.clone() for t in c.run_fwd()]
@@ -371,7 +395,8 @@ def lib():
 
 def args(**kw):
     a = dict(q=rn.Heads(FAKE, 640, 64, 8), k=rn.Heads(FAKE + 1024, 640, 64, 2),
-             gq=FAKE + (1 << 32), gk=FAKE + (1 << 32) + 4096, qo=rn.Heads(FAKE + (2 << 32), 512, 64, 8),
+             gq=FAKE + (1 << 32), gk=FAKE + (1 << 32) + 4096,
+             qo=rn.Heads(FAKE + (2 << 32), 512, 64, 8),
              ko=rn.Heads(FAKE + (3 << 32), 128, 64, 2), T=4, D=64, eps=1e-6, xd=1, wd=1,
              sections=[12, 10, 10], R=64, positions=FAKE + (4 << 32), pst=4,
              inv_freq=FAKE + (5 << 32), pairs=0, order=0, axes=None)
@@ -386,17 +411,22 @@ def args(**kw):
 
 H = rn.Heads
 REFUSED = [
-    (dict(q=None), 1), (dict(qo=None), 1), (dict(ko=None), 1), (dict(k=None), 1), (dict(gq=None), 1),
+    (dict(q=None), 1), (dict(qo=None), 1), (dict(ko=None), 1), (dict(k=None), 1),
+    (dict(gq=None), 1),
     (dict(gk=None), 1), (dict(rope=None), 1), (dict(T=-1), 1), (dict(T=1 << 30), 1), (dict(D=0), 1),
     (dict(D=8193), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(R=63), 1),
     (dict(R=0, sections=[0, 0, 0]), 1), (dict(R=66, sections=[13, 10, 10]), 1),
-    (dict(sections=[12, 10, 9]), 1), (dict(sections=[12, 10, 11]), 1), (dict(sections=[-2, 24, 10]), 1),
+    (dict(sections=[12, 10, 9]), 1), (dict(sections=[12, 10, 11]), 1),
+    (dict(sections=[-2, 24, 10]), 1),
     (dict(sections=[2, 20, 10], order=1), 1), (dict(axes=0), 1), (dict(axes=5), 1),
     (dict(pairs=2), 1), (dict(pairs=-1), 1), (dict(order=2), 1), (dict(pst=3), 1),
     (dict(positions=None), 1), (dict(inv_freq=None), 1), (dict(positions=FAKE + (4 << 32) + 4), 3),
     (dict(inv_freq=FAKE + (5 << 32) + 2), 3), (dict(q=H(FAKE + 1, 640, 64, 8)), 3),
     (dict(gq=FAKE + (1 << 32) + 1), 3), (dict(q=H(None, 640, 64, 8)), 1),
-    (dict(q=H(FAKE, 640, 32, 8)), 1), (dict(q=H(FAKE, 500, 64, 8)), 1), (dict(q=H(FAKE, -640, 64, 8)), 1),
+    (dict(q=H(FAKE, 640, 32, 8)), 1), (dict(q=H(FAKE, 500, 64, 8)), 1),
+    (dict(q=H(FAKE, -640, 64, 8)), 1),
+    (dict(q=H(FAKE, 64, 255, 8)), 1), (dict(q=H(FAKE, 63, 256, 8)), 1),   # heads first
+    (dict(q=H(FAKE, 256, 1 << 58, 8)), 1), (dict(pst=1 << 57), 1),
     (dict(q=H(FAKE, 640, 64, -8)), 1), (dict(q=H(FAKE, 640, 64, 7)), 1),
     (dict(q=H(FAKE, 1 << 62, 64, 8)), 1), (dict(q=H(FAKE, 640, 1 << 62, 8)), 1),
     (dict(q=H(FAKE, 1 << 23, 64, 1 << 17), qo=H(FAKE + (2 << 32), 1 << 23, 64, 1 << 17)), 1),
@@ -422,6 +452,10 @@ def test_forward_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(dq=None), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(ws=None), 4),
     (dict(ws=FAKE + (9 << 32) + 8), 4), (dict(dgq=FAKE + (7 << 32) + 2), 3),
+    (dict(k=H(FAKE, 640, 64, 0), dk=H(FAKE, 640, 64, 0), dxk=H(FAKE, 640, 64, 0),
+          dgk=FAKE + (7 << 32) + 5), 3),                # of no heads
+    (dict(k=H(FAKE, 640, 64, 0), dk=H(FAKE, 640, 64, 0), dxk=H(FAKE, 640, 64, 0),
+          dgk=FAKE + (7 << 32)), 1),
     (dict(dgk=FAKE + (7 << 32)), 1),                    # both gradients in one place
     (dict(dq=H(FAKE + (8 << 32), 512, 64, 7)), 1),
     (dict(dxq=H(FAKE, 640, 64, 8)), 1),                 # dq over q

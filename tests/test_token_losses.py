@@ -357,6 +357,37 @@ def test_policy_gradient_against_differences():
         assert abs(num - float(d[i, j])) <= 1e-8 + 1e-5 * abs(num)
 
 
+@gpu
+def test_a_wait_that_runs_out_is_reported(debug_env):
+    """A negative limit makes every wait of a cluster for its peers give up at once.  The
+    kernel has to end all the same, and the next call to be right."""
+    x, t, _ = rows(5, 65536, "bf16")
+    r = Ref(x, t, 1.0)
+    old, ref, A, w = policy_inputs(r)
+    want = policy(x, t, old, ref, A, w, 0.1, "bf16")
+    rn.rmsnorm_check_device()
+    debug_env.set("RMSNORM_WAIT_LIMIT_CYCLES", "-1")
+    policy(x, t, old, ref, A, w, 0.1, "bf16")
+    with pytest.raises(rn.RMSNormError) as e:
+        rn.rmsnorm_check_device()
+    assert e.value.status == 6                   # RMSNORM_ERR_TIMEOUT
+    debug_env.delete("RMSNORM_WAIT_LIMIT_CYCLES")
+    got = policy(x, t, old, ref, A, w, 0.1, "bf16")
+    rn.rmsnorm_check_device()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+def test_another_familys_forced_variant_is_none_of_theirs(debug_env):
+    x, t, _ = rows(40, 3000, "bf16")
+    r = Ref(x, t, 1.0)
+    old, ref, A, w = policy_inputs(r)
+    want = (*fwd(x, t, 1.0, "bf16"), *policy(x, t, old, ref, A, w, 0.1, "bf16"))
+    debug_env.set("RMSNORM_FORCE_VARIANT", "cta:t=512:cl=3")
+    got = (*fwd(x, t, 1.0, "bf16"), *policy(x, t, old, ref, A, w, 0.1, "bf16"))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ---------------------------------------------------------------- preference loss
 
 def preference(x, t, ref, cu, beta, ls, dt, inv_t=1.0, stream=None):

@@ -294,6 +294,21 @@ def test_arguments_are_checked_before_any_call():
 
 
 @gpu
+def test_last_tokens_of_long_sequences():
+    # rows far apart: their gradient takes the rows' own memory, not the stride's
+    x = torch.randn(2, 1500, 1001, device="cuda")
+    t = torch.tensor([5, 900], device="cuda")
+    rows = x[:, -1].detach().requires_grad_(True)
+    before = torch.cuda.memory_allocated()
+    d, = torch.autograd.grad(ag.token_logprobs(rows, t).sum(), rows)
+    assert torch.cuda.memory_allocated() - before < 1 << 17
+    p = torch.softmax(rows.double(), -1)
+    want = torch.nn.functional.one_hot(t, 1001) - p
+    # an exponent below 32 in two roundings, and the sum behind rel_lse: some 120 x 2^-24
+    assert bool(((d - want).abs() <= 2.0 ** -17 * p + 2.0 ** -22 * want.abs()).all())
+
+
+@gpu
 def test_wrong_shapes_are_refused():
     q, k = torch.randn(5, 4, 8, device="cuda"), torch.randn(5, 2, 8, device="cuda")
     pos, inv = torch.zeros(2, 5, dtype=torch.int64, device="cuda"), torch.ones(4, device="cuda")
@@ -307,6 +322,8 @@ def test_wrong_shapes_are_refused():
                 lambda: ag.rms_norm_rope(q, k, w, w.bfloat16(), pos, inv, [2, 2])):
         with pytest.raises(ValueError):
             bad()
+    with pytest.raises(ValueError):
+        ag.rms_norm_rope(q, k, None, w, pos, inv, [2, 2])
     with pytest.raises(rn.RMSNormError):
         ag.rms_norm_rope(q, k, w, None, pos, inv, [2, 2])
     x, t = torch.randn(3, 8, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
