@@ -1728,7 +1728,7 @@ void rope_shape(int64_t D, int64_t R, int xd, int align, bool norm_bwd, int* e_o
 // the SMs (kRopeItems of them when the rows allow), each of whole steps of
 // `step` rows.
 constexpr int64_t kRopeItems = 4096;
-constexpr int kRopeBlockSteps = 8;
+constexpr int kRopeBlockSteps = 4;
 void rope_chunks(int64_t T, int rows, int step, int* chunks, int* per_chunk) {
   const int64_t steps = (rows + step - 1) / step;
   int64_t c = T > 0 ? (kRopeItems + T - 1) / T : 1;
@@ -1896,13 +1896,27 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
   p.block = 1;
   if (g > 0) {
     const int step = 32 / g, warps = kRopeThreads / 32;
-    // Tokens per work item: where a token's rows are fewer than kRopeBlockSteps
-    // steps (in the backward: those of its longer view), so many that an item has
-    // that many -- its lanes full, its start-up shared -- as long as kRopeItems items
-    // remain and a warp's angles stay below 2 KB.
+    // Tokens per work item, as long as kRopeItems items remain and a warp's angles stay
+    // below 2 KB.  Forward: where a token's rows are fewer than two steps, so many that
+    // an item has those (2 heads of 128 bf16: 22037 tokens 12.3 us, one token an item
+    // 15.1; with two steps a token already blocks cost: 8 heads of 128, 9000 tokens 11.3,
+    // two tokens an item 15.7).  Backward, a view at a time: up to kRopeBlockSteps steps
+    // where the longer view has less than two (30000 tokens of 6 + 2 heads 53 us, one
+    // token an item 67), and until its steps' lanes are busy (16000 tokens of 28 + 4
+    // heads of 64 44, one token an item 48); others lose by it (8 + 8 heads of 128 45 us,
+    // two tokens an item 51).
     const int64_t most = norm_bwd ? (heads[0] > heads[1] ? heads[0] : heads[1])
                                   : heads[0] + heads[1];
-    while (l == 1 && p.block < kRopeMaxBlock && p.block * most < kRopeBlockSteps * step &&
+    const int64_t want = (norm_bwd && most < 2 * step ? kRopeBlockSteps : 2) * step;
+    auto lanes_idle = [&]() {   // in more than an eighth of the backward's steps
+      int64_t rows = 0, lanes = 0;
+      for (int i = 0; i < 2; ++i) {
+        rows += p.block * heads[i];
+        lanes += (p.block * heads[i] + step - 1) / step * step;
+      }
+      return norm_bwd && lanes * 8 > rows * 9;
+    };
+    while (l == 1 && p.block < kRopeMaxBlock && (p.block * most < want || lanes_idle()) &&
            T >= 2 * p.block * kRopeItems && p.block * R <= 256)
       p.block *= 2;
     const int64_t groups = (T + p.block - 1) / p.block;
@@ -1915,14 +1929,22 @@ rmsnorm_status_t rope_impl(bool bwd, const rmsnorm_heads_t* q, const rmsnorm_hea
       rope_chunks(groups, (int)(heads[0] + heads[1]), step, &p.chunks[0], &p.heads_per_chunk[0]);
       grid = (groups * p.chunks[0] + warps - 1) / warps;
     } else {
-      int64_t items = 0;
+      int64_t items = 0, apart = 0, split = 0;
       for (int i = 0; i < 2; ++i) {
         rope_chunks(groups, (int)heads[i], step, &p.chunks[i], &p.heads_per_chunk[i]);
         if (heads[i]) items += groups * p.chunks[i];
+        split = apart;
+        if (heads[i]) apart += (groups * p.chunks[i] + warps - 1) / warps;
       }
       grid = (items + warps - 1) / warps;
       if (grid > 2 * di.sms) grid = 2 * di.sms;
       if (grid > ctas) grid = ctas;
+      // q and k side by side instead of one after the other (33 tokens of 32 heads of
+      // 256: 6.5 us against 8.6), where the CTAs for that are there
+      if (heads[0] && heads[1] && apart <= 2 * di.sms && apart <= ctas) {
+        grid = apart;
+        p.split = (int)split;
+      }
     }
   } else {
     const int64_t steps = D - R / 2;   // columns or pairs a row's threads share
@@ -2173,10 +2195,13 @@ rmsnorm_status_t token_logprob_bwd_impl(const void* logits, int64_t ld, const in
   p.dlogits = dlogits;
   p.ld_out = ld_out;
   p.whole_rows = dlogits == logits;
-  const int64_t per = p.whole_rows ? V : (int64_t)kLossBwdVecs * per_vec(xd);
+  // as many threads as a row has batches of vectors
+  int threads = 32;
+  while (threads < kLossThreads && (int64_t)threads * kLossBatch * per_vec(xd) < V) threads *= 2;
+  const int64_t per = p.whole_rows ? V : (int64_t)threads * kLossBatch * per_vec(xd);
   const int64_t items = M * ((V + per - 1) / per), cap = int64_t(1) << 30;
-  return launch_loss(xd == kF32 ? get_loss_bwd_f32() : get_loss_bwd_bf16(),
-                     items < cap ? items : cap, kLossThreads, p, stream,
+  return launch_loss(xd == kF32 ? get_loss_bwd_f32(threads) : get_loss_bwd_bf16(threads),
+                     items < cap ? items : cap, threads, p, stream,
                      "logits gradient launch");
 }
 

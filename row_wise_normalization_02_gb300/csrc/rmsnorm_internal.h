@@ -252,6 +252,8 @@ struct RopeParams {
   int chunks[2];             // work items per token: chunks of heads_per_chunk heads (forward:
   int heads_per_chunk[2];    //   [0] covers the rows of q and k together)
   int block;                 // or, where rows are few, tokens per work item (one chunk)
+  int split;                 // backward with the norm: the CTAs before this one take q, the
+                             // others k (0: all take both)
   float* partial;            // backward with the norm: [gridDim.x][2 * ld_half], or null
   int ld_half;
 };
@@ -315,8 +317,8 @@ using LossKernel = void (*)(LossParams);
 // CTAs of `threads` threads with rings of `stages` batches).
 LossKernel get_loss_rows_f32(int mode, int cluster, int threads, int stages);
 LossKernel get_loss_rows_bf16(int mode, int cluster, int threads, int stages);
-LossKernel get_loss_bwd_f32();
-LossKernel get_loss_bwd_bf16();
+LossKernel get_loss_bwd_f32(int threads);
+LossKernel get_loss_bwd_bf16(int threads);
 LossKernel get_loss_sum();        // loss = sum of token_loss, one CTA
 LossKernel get_loss_pairs();      // one CTA per pair: margins, dlogp
 LossKernel get_loss_pairs_all();  // one CTA: margins, dlogp and loss
@@ -325,7 +327,6 @@ constexpr int kLossThreads = 256;  // at most: eight warps
 constexpr int kLossBatch = 4;     // 16-byte vectors a thread takes at a time
 constexpr int kLossStages = 4;    // batches in a thread's ring (loss with gradient)
 constexpr int loss_stages(int threads) { return threads == 32 ? 2 : kLossStages; }
-constexpr int kLossBwdVecs = kLossThreads * kLossBatch;   // vectors of a row per backward CTA
 
 // Threads per CTA of the subwarp families; upper bound of the per-row CTAs.
 constexpr int kSubwarpThreads = 256;

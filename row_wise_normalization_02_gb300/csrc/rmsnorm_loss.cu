@@ -766,18 +766,18 @@ __global__ void __launch_bounds__(NT, 896 / NT) loss_stream_kernel(LossParams p)
 // unlikely that this would lose digits (rel > kRelFine), or has no probability at
 // all, a CTA takes its row's maximum and sum again and uses those.
 //
-// A CTA takes kLossBwdVecs vectors of a row -- or (p.whole_rows: dlogits is logits, whose
+// A CTA takes kLossBatch vectors a thread of a row -- or (p.whole_rows: dlogits is logits, whose
 // target another CTA might overwrite) a whole row.  Rows that take no part and
 // rows whose g is zero are zeroed without being read.
 constexpr float kRelFine = 64.f;
-template <typename TX>
-__global__ void __launch_bounds__(kLossThreads, 4) loss_bwd_kernel(LossParams p) {
-  constexpr int E = Elem<TX>::kPerVec, U = kLossBatch;
+template <typename TX, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) loss_bwd_kernel(LossParams p) {
+  constexpr int E = Elem<TX>::kPerVec, U = kLossBatch, per = U * NT;
   __shared__ Run part[32];
   __shared__ Run again;
   pdl_begin();
   const int tid = threadIdx.x;
-  const int chunks = (p.V + kLossBwdVecs * E - 1) / (kLossBwdVecs * E);
+  const int chunks = (p.V + per * E - 1) / (per * E);
   const int per_row = p.whole_rows ? 1 : chunks;
   const int64_t items = p.M * per_row;
   const float scale = (p.scale ? *p.scale : 1.f) * p.inv_tf;
@@ -798,14 +798,14 @@ __global__ void __launch_bounds__(kLossThreads, 4) loss_bwd_kernel(LossParams p)
     // chunks of the row's vectors; the last one is short by the head at most, so
     // the row's `chunks` chunks cover them all
     const Frame f = frame_of(x, p.V);
-    int w0 = c0 * kLossBwdVecs + tid;
+    int w0 = c0 * per + tid;
     uint4 b[U];
     auto load = [&]() {
       if (g != 0.f && alike) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          if (w0 + k * kLossThreads < f.nvec)
-            b[k] = ld_rw(x + f.head + (size_t)(w0 + k * kLossThreads) * E);
+          if (w0 + k * NT < f.nvec)
+            b[k] = ld_rw(x + f.head + (size_t)(w0 + k * NT) * E);
       }
     };
     load();   // on their way while the target's logit is
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(kLossThreads, 4) loss_bwd_kernel(LossParams p)
         d.at = -g * expm1f(-rel);
       } else {
         Run r{kNegInf, 0.f, 0.f};
-        for (int j = tid; j < p.V; j += kLossThreads) add_one(r, ld_scalar(x + j), sc);
+        for (int j = tid; j < p.V; j += NT) add_one(r, ld_scalar(x + j), sc);
         r = cta_merge(r, sc, part);
         if (tid == 0) again = r;
         __syncthreads();
@@ -830,8 +830,8 @@ __global__ void __launch_bounds__(kLossThreads, 4) loss_bwd_kernel(LossParams p)
         __syncthreads();   // xt has been read; and `part`, `again` before another item
     }
     if (!alike) {
-      const int e1 = min((int64_t)p.V, (int64_t)c1 * kLossBwdVecs * E);
-      for (int j = c0 * kLossBwdVecs * E + tid; j < e1; j += kLossThreads)
+      const int e1 = min((int64_t)p.V, (int64_t)c1 * per * E);
+      for (int j = c0 * per * E + tid; j < e1; j += NT)
         put_one<TX, true>(dx + j, g == 0.f ? 0.f : ld_scalar(x + j), d, j == t);
       continue;
     }
@@ -839,21 +839,21 @@ __global__ void __launch_bounds__(kLossThreads, 4) loss_bwd_kernel(LossParams p)
     for (;;) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int w = w0 + k * kLossThreads;
+        const int w = w0 + k * NT;
         if (w >= f.nvec) break;
         st_stream(dx + f.head + (size_t)w * E,
                   g == 0.f ? make_uint4(0, 0, 0, 0) : gradient<TX, true>(b[k], d, tv - w * E));
       }
-      w0 += kLossBwdVecs;
-      if (w0 >= c1 * kLossBwdVecs) break;
+      w0 += per;
+      if (w0 >= c1 * per) break;
       load();
     }
     if (chunk == 0) {
       auto element = [&](int j) {
         put_one<TX, true>(dx + j, g == 0.f ? 0.f : ld_scalar(x + j), d, j == t);
       };
-      for (int j = tid; j < f.head; j += kLossThreads) element(j);
-      for (int j = f.tail0 + tid; j < p.V; j += kLossThreads) element(j);
+      for (int j = tid; j < f.head; j += NT) element(j);
+      for (int j = f.tail0 + tid; j < p.V; j += NT) element(j);
     }
   }
 }
@@ -1034,6 +1034,15 @@ LossKernel pick_stream(int cluster, int threads, int stages) {
   }
 }
 template <typename TX>
+LossKernel pick_bwd(int threads) {
+  switch (threads) {
+    case 32: return loss_bwd_kernel<TX, 32>;
+    case 64: return loss_bwd_kernel<TX, 64>;
+    case 128: return loss_bwd_kernel<TX, 128>;
+    default: return loss_bwd_kernel<TX, 256>;
+  }
+}
+template <typename TX>
 LossKernel pick_mode(int mode, int cluster, int threads, int stages) {
   switch (mode) {
     case kLossLogprob: return pick_row<TX, kLossLogprob>(cluster);
@@ -1050,7 +1059,7 @@ LossKernel pick_mode(int mode, int cluster, int threads, int stages) {
 LossKernel get_loss_rows_f32(int mode, int cluster, int threads, int stages) {
   return pick_mode<float>(mode, cluster, threads, stages);
 }
-LossKernel get_loss_bwd_f32() { return loss_bwd_kernel<float>; }
+LossKernel get_loss_bwd_f32(int threads) { return pick_bwd<float>(threads); }
 LossKernel get_loss_sum() { return loss_sum_kernel; }
 LossKernel get_loss_pairs() { return loss_pairs_kernel; }
 LossKernel get_loss_pairs_all() { return loss_pairs_all_kernel; }
@@ -1059,7 +1068,7 @@ LossKernel get_loss_pairs_mean() { return loss_pairs_mean_kernel; }
 LossKernel get_loss_rows_bf16(int mode, int cluster, int threads, int stages) {
   return pick_mode<bf16>(mode, cluster, threads, stages);
 }
-LossKernel get_loss_bwd_bf16() { return loss_bwd_kernel<bf16>; }
+LossKernel get_loss_bwd_bf16(int threads) { return pick_bwd<bf16>(threads); }
 #endif
 
 }  // namespace rmsn

@@ -332,6 +332,44 @@ __device__ __forceinline__ void load_gamma(const void* gamma, int vec, float (&w
   }
 }
 
+// Two bf16 products, exact in fp32, from the packed halves by the mixed-precision fma
+// (addend -0 keeps a zero's sign) ...
+__device__ __forceinline__ float2 products(uint32_t x, uint32_t w) {
+  float2 r;
+  asm("{\n\t.reg .b16 xl, xh, wl, wh;\n\t"
+      "mov.b32 {xl, xh}, %2;\n\t"
+      "mov.b32 {wl, wh}, %3;\n\t"
+      "fma.rn.f32.bf16 %0, xl, wl, 0f80000000;\n\t"
+      "fma.rn.f32.bf16 %1, xh, wh, 0f80000000;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(x), "r"(w));
+  return r;
+}
+// ... and two running sums of squares.
+__device__ __forceinline__ void add_squares(float2& acc, uint32_t x) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, l, l, %0;\n\t"
+      "fma.rn.f32.bf16 %1, h, h, %1;\n\t}"
+      : "+f"(acc.x), "+f"(acc.y)
+      : "r"(x));
+}
+__device__ __forceinline__ void add_squares(float2& acc, const uint4& v) {
+  add_squares(acc, v.x);
+  add_squares(acc, v.y);
+  add_squares(acc, v.z);
+  add_squares(acc, v.w);
+}
+// x gamma rstd of a vector, so.
+template <int E>
+__device__ __forceinline__ void scale_packed(float (&o)[E], const uint4& x, const uint4& w,
+                                             float rstd) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i)
+    put_pair(o, 2 * i, __fmul2_rn(products(xs[i], ws[i]), make_float2(rstd, rstd)));
+}
+
 // Lane 4 k + a holds the position of token t0 + k on axis a (of up to eight
 // tokens), so that it can be asked for long before it is needed.
 __device__ __forceinline__ long long lane_position(const RopeParams& p, int64_t t0, int tokens) {
@@ -394,7 +432,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
   using V = Raw<B>;
   extern __shared__ float4 smem4[];
   pdl_begin();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // in a uniform register
   const int g = lane % G, rg = lane / G;
   V* ring = reinterpret_cast<V*>(smem4) + tid;   // [S][2 L][threads]
   const uint32_t item = blockIdx.x * (kRopeThreads / 32) + warp;
@@ -423,12 +462,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
   const TX* xk = static_cast<const TX*>(p.v[1].x) + t0 * p.v[1].x_st;
   TX* yq = static_cast<TX*>(p.v[0].y) + t0 * p.v[0].y_st;
   TX* yk = static_cast<TX*>(p.v[1].y) + t0 * p.v[1].y_st;
+  // The lane's row of a step, RG rows further with every step (and from q to k); worked
+  // out for every row where lanes hold several units (16000 tokens of 32 heads of 36
+  // bf16: 26 us, stepped on 31).
+  constexpr bool STEPPED = !BLOCK && L == 1;
+  auto row_of = [&](const RopeView& v, const TX* base, int r, bool out) {
+    return base + r * (out ? v.y_sh : v.x_sh);
+  };
+  auto further = [&](const TX* at, int r, const TX* k0, bool out) {   // r: the new row
+    if (r >= nq && r < nq + RG) return row_of(p.v[1], k0, r - nq, out);
+    const RopeView& v = p.v[r >= nq];
+    return at + RG * (out ? v.y_sh : v.x_sh);
+  };
+  int r_in = h0 + rg, r_out = r_in;
+  const TX* x_row = r_in < nq ? row_of(p.v[0], xq, r_in, false)
+                              : row_of(p.v[1], xk, r_in - nq, false);
+  const TX* y_row = r_in < nq ? row_of(p.v[0], yq, r_in, true)
+                              : row_of(p.v[1], yk, r_in - nq, true);
   auto load = [&](int stage, int j) {
     if (j < total) {
-      int tok, r;
-      place(j, &tok, &r);
-      const TX* x = r < nq ? xq + r * p.v[0].x_sh : xk + (r - nq) * p.v[1].x_sh;
-      if (BLOCK) x += tok * (r < nq ? p.v[0].x_st : p.v[1].x_st);
+      const TX* x = x_row;
+      if (!STEPPED) {
+        int tok, r;
+        place(j, &tok, &r);
+        x = r < nq ? xq + r * p.v[0].x_sh + tok * p.v[0].x_st
+                   : xk + (r - nq) * p.v[1].x_sh + tok * p.v[1].x_st;
+      }
       V* slot = ring + stage * (2 * L * kRopeThreads);
 #pragma unroll
       for (int k = 0; k < L; ++k)
@@ -438,6 +497,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
         }
     }
     copy_commit();
+    if (STEPPED) x_row = further(x_row, r_in += RG, xk, false);
   };
   // the first rows are on their way while the angles are computed
 #pragma unroll
@@ -455,6 +515,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
   int at = -1;   // the token whose angles cs holds
   if (!BLOCK) angles_at(0);
   int stage = 0;
+  // bf16 with bf16 weights: squares and products with gamma straight from the packed words
+  constexpr bool PACKED = NORM && B == 16 && sizeof(TX) == 2 && sizeof(TW) == 2;
   for (int j0 = 0; j0 < total; j0 += RG) {
     const int j = j0 + rg;
     int tok, r;
@@ -467,9 +529,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
     copy_wait<S - 1>();
     const V* slot = ring + stage * (2 * L * kRopeThreads);
     float a[L][E], b[L][E];
+    V xa[L], xb[L];
     float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < L; ++k) {
+      if constexpr (PACKED) {
+        xa[k].v = xb[k].v = make_uint4(0, 0, 0, 0);
+        if (live && g + k * G < units) {
+          xa[k] = slot_of(slot + 2 * k * kRopeThreads);
+          xb[k] = slot_of(slot + (2 * k + 1) * kRopeThreads);
+        }
+        add_squares(ss, xa[k].v);
+        add_squares(ss, xb[k].v);
+        continue;
+      }
       if (live && g + k * G < units) {
         unpack_raw(slot_of(slot + 2 * k * kRopeThreads), a[k]);
         unpack_raw(slot_of(slot + (2 * k + 1) * kRopeThreads), b[k]);
@@ -486,13 +559,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
     stage = stage + 1 == S ? 0 : stage + 1;
     float rstd = 1.f;
     if (NORM) rstd = rsqrtf(group_sum<G>(ss.x + ss.y) * p.inv_d + p.eps);
+    TX* y_at = const_cast<TX*>(y_row);
+    if (STEPPED) y_row = further(y_row, r_out += RG, yk, true);
     if (!live) continue;
-    TX* y = r < nq ? yq + r * p.v[0].y_sh : yk + (r - nq) * p.v[1].y_sh;
-    if (BLOCK) y += tok * (r < nq ? p.v[0].y_st : p.v[1].y_st);
+    TX* y = y_at;
+    if (!STEPPED)
+      y = r < nq ? yq + r * p.v[0].y_sh + tok * p.v[0].y_st
+                 : yk + (r - nq) * p.v[1].y_sh + tok * p.v[1].y_st;
 #pragma unroll
     for (int k = 0; k < L; ++k) {
       if (g + k * G >= units) continue;
-      if (NORM) {   // gamma from L1: in registers it would cost a CTA per SM (116 us for 105)
+      if constexpr (PACKED) {
+        const TW* w = static_cast<const TW*>(r < nq ? p.v[0].gamma : p.v[1].gamma);
+        scale_packed(a[k], xa[k].v, ld_cached(w + va[k] * E), rstd);
+        scale_packed(b[k], xb[k].v, ld_cached(w + vb[k] * E), rstd);
+      } else if (NORM) {   // gamma from L1: in registers it would cost a CTA per SM (116 us for 105)
         float w[E];
         load_gamma<TX, TW>(r < nq ? p.v[0].gamma : p.v[1].gamma, va[k], w);
         scale_all(w, w, rstd);
@@ -513,14 +594,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
 // its rows, or a block of tokens) of q, then those of k, its lanes keeping the
 // dgamma partials of their columns in registers; after each view the CTA adds its
 // lanes' partials in a fixed order into its partial row.  The ring runs on from
-// item to item, and so do the positions, one item ahead.
+// item to item, and so do the positions, one item ahead.  Small batches, whose items
+// take each warp one round at most: the first p.split CTAs take q, the others k.
 template <typename TX, typename TW, int E, int G, int L, bool ADJ, bool BLOCK>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopeParams p) {
   constexpr int RG = 32 / G, W = kRopeThreads / 32, B = E * sizeof(TX), S = kRopeBwdSteps;
   using V = Raw<B>;
   extern __shared__ float4 smem4[];
   pdl_begin();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // in a uniform register
   const int g = lane % G, rg = lane / G;
   const int units = p.D / (2 * E);
   int va[L], vb[L];
@@ -531,14 +614,16 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
                                         S * 4 * L * kRopeThreads);    // [W][D rounded to 4]
   const int ld_red = (p.D + 3) & ~3;
   const Tables tab = make_tables(p, red + W * ld_red);
-  const uint32_t nw = gridDim.x * W, w0 = blockIdx.x * W + warp;
+  const bool apart = p.split > 0, latter = apart && blockIdx.x >= (unsigned)p.split;
+  const uint32_t cta0 = latter ? p.split : 0, cta1 = apart && !latter ? p.split : gridDim.x;
+  const uint32_t nw = (cta1 - cta0) * W, w0 = (blockIdx.x - cta0) * W + warp;
   const int block = BLOCK ? p.block : 1;
   const uint32_t groups = (uint32_t)((p.T + block - 1) / block);
   uint32_t skip = 0;   // items of q, so that k's start where q's ended
 
   for (int side = 0; side < 2; ++side) {
     const RopeView& v = p.v[side];
-    if (v.heads == 0) {   // an absent view: its partial columns are zero
+    if (v.heads == 0 || (apart && side != (int)latter)) {   // its partial columns are zero
       if (p.partial)
         for (int d = tid; d < p.ld_half; d += kRopeThreads)
           p.partial[(size_t)blockIdx.x * 2 * p.ld_half + side * p.ld_half + d] = 0.f;
@@ -583,15 +668,30 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
     uint32_t it = (w0 + nw - skip % nw) % nw, f_it = it;
     int f_j = 0;
     Item f{};
-    if (f_it < items) f = item_at(f_it);
+    // The lane's row of a step, stepped on where rows are wide (8000 tokens of 32 heads of
+    // 192 bf16: 64 us, worked out for every row 68; heads of 128 and 32768 tokens 176
+    // against 164)
+    constexpr bool STEPPED = !BLOCK && G >= 16;
+    const TX *fx = nullptr, *fd = nullptr;
+    auto start = [&]() {
+      f = item_at(f_it);
+      if (STEPPED) {
+        fx = static_cast<const TX*>(v.x) + f.t0 * v.x_st + (f.h0 + rg) * v.x_sh;
+        fd = static_cast<const TX*>(v.dy) + f.t0 * v.dy_st + (f.h0 + rg) * v.dy_sh;
+      }
+    };
+    if (f_it < items) start();
     auto load = [&](int stage) {
       if (f_it < items) {
         const int j = f_j + rg;
         if (j < f.tokens * f.rows) {
-          int tok, h;
-          place(f, j, &tok, &h);
-          const TX* xr = static_cast<const TX*>(v.x) + (f.t0 + tok) * v.x_st + h * v.x_sh;
-          const TX* dr = static_cast<const TX*>(v.dy) + (f.t0 + tok) * v.dy_st + h * v.dy_sh;
+          const TX *xr = fx, *dr = fd;
+          if (!STEPPED) {
+            int tok, h;
+            place(f, j, &tok, &h);
+            xr = static_cast<const TX*>(v.x) + (f.t0 + tok) * v.x_st + h * v.x_sh;
+            dr = static_cast<const TX*>(v.dy) + (f.t0 + tok) * v.dy_st + h * v.dy_sh;
+          }
           V* slot = ring + stage * (4 * L * kRopeThreads);
 #pragma unroll
           for (int k = 0; k < L; ++k)
@@ -603,10 +703,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
             }
         }
         f_j += RG;
+        fx += RG * v.x_sh;
+        fd += RG * v.dy_sh;
         if (f_j >= f.tokens * f.rows) {
           f_j = 0;
           f_it += nw;
-          if (f_it < items) f = item_at(f_it);
+          if (f_it < items) start();
         }
       }
       copy_commit();
@@ -635,7 +737,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
       int at = -1;   // the token whose angles cs holds
       if (!BLOCK) angles_at(0);
       const int total = m.tokens * m.rows;
-      for (int j0 = 0; j0 < total; j0 += RG) {
+      TX* yr = static_cast<TX*>(v.y) + m.t0 * v.y_st + (m.h0 + rg) * v.y_sh;
+      for (int j0 = 0; j0 < total; j0 += RG, yr += RG * v.y_sh) {
         const int j = j0 + rg;
         int tok, h;
         place(m, j, &tok, &h);
@@ -682,7 +785,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
         }
         const float c = r * r * p.inv_d * group_sum<G>(dot.x + dot.y);
         if (!live) continue;
-        TX* y = static_cast<TX*>(v.y) + (m.t0 + tok) * v.y_st + h * v.y_sh;
+        TX* y = STEPPED ? yr : static_cast<TX*>(v.y) + (m.t0 + tok) * v.y_st + h * v.y_sh;
 #pragma unroll
         for (int k = 0; k < L; ++k) {
           if (g + k * G >= units) continue;
