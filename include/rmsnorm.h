@@ -340,7 +340,8 @@ typedef enum rmsnorm_rope_order {
  */
 typedef struct rmsnorm_rope {
   const int64_t* positions;  /* [axes, T] */
-  int64_t positions_stride;  /* elements from one axis to the next, T .. 2^56 when axes > 1 */
+  int64_t positions_stride;  /* elements from one axis to the next: T .. 2^56, or 0 for
+                                the same positions on every axis; unused for one axis */
   const float* inv_freq;     /* [R / 2] */
   int64_t rotary_dim;        /* R: even, 2 <= R <= D */
   int32_t axes;              /* 1 .. RMSNORM_ROPE_MAX_AXES */

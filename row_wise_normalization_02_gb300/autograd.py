@@ -29,6 +29,11 @@ The rotary functions take q and k as [..., H, D] views with a contiguous last
 dimension (slices of a fused projection are read in place) and the losses take
 logits as [..., V] with the row stride they come with (a padded vocabulary's
 slice is read in place); other layouts are copied first.
+
+A step of these can be captured into a CUDA graph, backward included, after one run
+on a side stream.  Let go of that run's losses first: an eager graph that still holds
+the same parameters ties their gradients to its own stream, which a capture cannot
+wait for.
 """
 from __future__ import annotations
 
@@ -259,6 +264,8 @@ def _apply_rope(q, k, q_gamma, k_gamma, positions, inv_freq, sections, pairs, or
     if positions.shape != want and not (len(sections) == 1 and positions.shape == lead):
         raise ValueError(f"positions must be {want}, a row for each axis")
     positions = positions.reshape(len(sections), -1)
+    if positions.stride(1) != 1 or 0 < positions.stride(0) < positions.shape[1]:
+        positions = positions.contiguous()
     out = _Rope.apply(_rows_of_heads(q), None if k is None else _rows_of_heads(k), q_gamma,
                       k_gamma, positions, inv_freq.contiguous(), sections, rotary_dim, pairs,
                       order, float(eps))

@@ -30,6 +30,7 @@
 
 #include "../../include/rmsnorm.h"
 #include "rmsnorm_internal.h"
+#include "rmsnorm_operators.h"
 #include "rmsnorm_wide_layout.h"
 
 namespace rmsn {
@@ -1629,8 +1630,8 @@ rmsnorm_status_t check_rope(const rmsnorm_rope_t* r, int64_t T, int64_t D) {
       return RMSNORM_ERR_INVALID_ARG;
     sum += n;
   }
-  if (sum != half || (r->axes > 1 && (r->positions_stride < T ||
-                                      r->positions_stride > (int64_t(1) << 56))))
+  const int64_t ps = r->axes > 1 ? r->positions_stride : 0;
+  if (sum != half || (ps != 0 && ps < T) || ps > (int64_t(1) << 56))
     return RMSNORM_ERR_INVALID_ARG;
   if (T == 0) return RMSNORM_OK;
   if (!r->positions || !r->inv_freq) return RMSNORM_ERR_INVALID_ARG;

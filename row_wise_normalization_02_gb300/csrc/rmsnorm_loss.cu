@@ -25,6 +25,7 @@
 
 #include "rmsnorm_device.cuh"
 #include "rmsnorm_internal.h"
+#include "rmsnorm_operators.h"
 #include "rmsnorm_ring.cuh"   // kDrainLimit
 
 #ifndef RMSN_PAIR
@@ -100,16 +101,18 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 struct Scale {
   float hi, lo;
 };
-// exp of a scaled difference of logits
+// exp of a scaled difference of logits (the exponent rounded once)
 __device__ __forceinline__ float term(float d, const Scale& c) {
-  return ex2(fmaf(d, c.lo, __fmul_rn(d, c.hi)));
+  return ex2(fmaf(d, c.hi, __fmul_rn(d, c.lo)));
 }
 // ex2.approx reads low by 5.0e-8 on average over every octave (2^20 arguments
-// each on a GB300; largest error 1.4e-7), and is exact at 0.  The sum of a row's
-// many terms shares that, and so would the log-probabilities of a whole
-// sequence: log_sum puts it back for all but the maximum's own 2^0.  (8192 rows of
-// 65536 normal logits: log s off by -6e-8 on average without, -1e-8 with.)
-constexpr float kEx2Low = 5.0e-8f;
+// each on a GB300; largest error 1.4e-7), and is exact at 0.  A row's many terms
+// share that, each rescaling of a sum adds its own, and the log-probabilities of a
+// whole sequence would add it up.  So raise and log_sum put back what rows show of it,
+// 3.8e-8 (4096 rows each of 1000 to 65536 normal logits, bf16 and fp32, at four
+// temperatures: logp off by 4e-8 to 1.3e-7 on average without, by 6e-9 with, at most
+// 2e-8; with 5.0e-8 by 2 to 6e-8 the other way).
+constexpr float kEx2Low = 3.8e-8f;
 
 // Maximum of U 16-byte vectors.  A NaN is passed over here and shows in the sum.
 template <int U>
@@ -156,7 +159,7 @@ __device__ __forceinline__ float origin(float m) { return m == kNegInf ? 0.f : m
 __device__ __forceinline__ void raise(Run& r, float m, const Scale& c) {
   if (m > r.m) {
     const float f = term(r.m - m, c), s = __fmul_rn(r.s, f);
-    r.e = fmaf(r.e, f, __fmaf_rn(r.s, f, -s));
+    r.e = fmaf(r.e, f, fmaf(s, kEx2Low, __fmaf_rn(r.s, f, -s)));
     r.s = s;
     r.m = m;
   }
@@ -202,7 +205,7 @@ __device__ __forceinline__ float sum_batch(const uint4 (&b)[U], float o, const S
     differences(b[k], o, d);
 #pragma unroll
     for (int i = 0; i < H; ++i) {
-      const float2 a = fma2(d[i], lo, mul2(d[i], hi));
+      const float2 a = fma2(d[i], hi, mul2(d[i], lo));
       s[i & 1] = add2(s[i & 1], make_float2(ex2(a.x), ex2(a.y)));
     }
   }
@@ -367,7 +370,7 @@ __device__ __forceinline__ PolicyTerm policy_term(const LossParams& p, const Row
 template <int MODE>
 __device__ __forceinline__ Grad finish_row(const LossParams& p, int64_t row, const Run& r,
                                            float xt, const RowIn& in, bool write) {
-  Grad verdict{};
+  Grad row_grad{};
   const Two ls = log_sum(r);
   const Two logp = minus(scaled(two_sum(xt, -r.m, 0.f), p), ls);
   if (write) {
@@ -382,13 +385,13 @@ __device__ __forceinline__ Grad finish_row(const LossParams& p, int64_t row, con
     }
     const float g = q.slope * p.inv_tf;
     if (MODE == kLossPolicyGrad)
-      verdict = Grad{g == 0.f ? 0.f : __fdividef(-g, r.s), origin(r.m), 0.f,
+      row_grad = Grad{g == 0.f ? 0.f : __fdividef(-g, r.s), origin(r.m), 0.f,
                      -g * expm1f(value_of(logp)), g, Scale{p.c_hi, p.c_lo}};
   }
   if (MODE == kLossPreference && write)
     p.dlogp[row] = row >= in.begin && row < in.end
                        ? value_of(minus(logp, Two{in.ref_logp, 0.f})) : 0.f;
-  return verdict;
+  return row_grad;
 }
 template <int MODE>
 __device__ __forceinline__ void left_out(const LossParams& p, int64_t row) {
@@ -517,11 +520,11 @@ __device__ __forceinline__ void copy_wait() {
 // to fetch), so the data a step needs is always the S-th last group.
 //
 // What bounds it.  DRAM would take 285 us for 4096 x 131072 bf16 with a fifth of the
-// rows left out; this takes 349 (5.5 TB/s).  A CTA's passes are short, and its
+// rows left out; this takes 343 (5.6 TB/s).  A CTA's passes are short, and its
 // merges, the exchange with its peers and the loss between them -- some 8000 of a
 // row's 25000 clocks -- leave its warps idle, so an SM needs many CTAs at different
-// points: 896 threads of it in CTAs as small as a row's part allows, the 64 bytes of
-// ring for a thread and batch being what 227 KB hold.  (One CTA of 1024 threads per
+// points: 768 threads of it (896 where the ring is shorter) in CTAs as small as a
+// row's part allows, the ring of 64 bytes a thread and batch being what 227 KB hold.  (One CTA of 1024 threads per
 // SM with the same ring 377 us; three quarters of a row in the ring 362.)  An SM
 // stores at most 32 bytes a clock, from wherever: 4.4 us for a row of 256 KB.
 template <typename TX, int NT, int CL, int S>
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(NT, 896 / NT) loss_stream_kernel(LossParams p)
   __shared__ float4 peers[2][8];   // m, s, e and, from the CTA that has it, the target's logit
   __shared__ uint64_t bar[2];
   __shared__ float target_logit;
-  __shared__ Grad verdict;
+  __shared__ Grad row_grad;
   __shared__ int stop;
   pdl_begin();
   const int tid = threadIdx.x;
@@ -709,10 +712,10 @@ __global__ void __launch_bounds__(NT, 896 / NT) loss_stream_kernel(LossParams p)
       }
     }
     ++turn;
-    if (tid == 0) verdict = finish_row<MODE>(p, row, r, xt, in, first);
+    if (tid == 0) row_grad = finish_row<MODE>(p, row, r, xt, in, first);
     __syncthreads();
     if (CL > 1 && stop) break;   // the peers give up the same way
-    const Grad d = verdict;
+    const Grad d = row_grad;
     if (!twice) {
       base = stage;
       for (int j = f.e0 + tid; j < f.e1; j += NT)

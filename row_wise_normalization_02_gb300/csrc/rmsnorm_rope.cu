@@ -32,6 +32,7 @@
 // flight through the arithmetic and no barrier waits for them.
 #include "rmsnorm_device.cuh"
 #include "rmsnorm_internal.h"
+#include "rmsnorm_operators.h"
 
 #ifndef RMSN_PAIR
 #error "compile once per dtype pair with -DRMSN_PAIR=0 (f32/f32), 1 (bf16/bf16), 2 (bf16/f32)"
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
         const TW* w = static_cast<const TW*>(r < nq ? p.v[0].gamma : p.v[1].gamma);
         scale_packed(a[k], xa[k].v, ld_cached(w + va[k] * E), rstd);
         scale_packed(b[k], xb[k].v, ld_cached(w + vb[k] * E), rstd);
-      } else if (NORM) {   // gamma from L1: in registers it would cost a CTA per SM (116 us for 105)
+      } else if (NORM) {   // gamma from L1: in registers it costs a CTA per SM (116 us for 105)
         float w[E];
         load_gamma<TX, TW>(r < nq ? p.v[0].gamma : p.v[1].gamma, va[k], w);
         scale_all(w, w, rstd);

@@ -311,6 +311,23 @@ def test_no_rows():
 
 
 @gpu
+@pytest.mark.parametrize("norm", [False, True])
+def test_tokens_further_apart_than_32_bits(norm):
+    c = Case(3, 4, 2, 64, 64, [12, 10, 10], layout="apart", norm=norm)
+    stride = (1 << 31) + 8
+    far = torch.empty(2 * stride + (4 << 20), dtype=torch.bfloat16, device="cuda")
+    for name in ("q", "k", "dyq", "dyk"):
+        t = getattr(c, name)
+        at = {"q": 0, "k": 1 << 20, "dyq": 2 << 20, "dyk": 3 << 20}[name]
+        v = far.as_strided(t.shape, (stride, 64, 1), at)
+        v.copy_(t)
+        setattr(c, name, v)
+    check_case(c)
+    c.in_place = True
+    check_case(c)
+
+
+@gpu
 def test_a_view_of_no_heads_has_a_zero_gradient():
     for D in (64, 2050):      # the vectors' kernel and the scalar one
         c = Case(5, 3, 2, D, D, [D // 2], layout="apart")

@@ -358,6 +358,30 @@ def test_policy_gradient_against_differences():
 
 
 @gpu
+def test_rows_further_apart_than_32_bits():
+    # 8.6 GB apart, of which only the rows are touched
+    M, V, ld = 3, 1003, (1 << 31) + 5
+    x, t, _ = rows(M, V, "bf16")
+    t[1] = 1002
+    r = Ref(x, t, 1.0)
+    old, ref, A, w = policy_inputs(r)
+    far = torch.empty((M - 1) * ld + V, dtype=torch.bfloat16, device="cuda")
+    far = far.as_strided((M, V), (ld, 1))
+    far.copy_(x)
+    logp, lse = fwd(far, t)
+    close(logp, r.logp, logp_tol(V) + U * r.logp.abs())
+    near = torch.empty(M, V + 1, dtype=torch.bfloat16, device="cuda")[:, :V]
+    _, _, _, lse, dlogp, _ = policy(far, t, old, ref, A, w, 0.1, "bf16", out=near)
+    want = near.clone()
+    policy(far, t, old, ref, A, w, 0.1, "bf16", out=far)      # in place
+    _, slope, tol = policy_ref(r, old, ref, A, w, 0.1)
+    for got in (want, far):
+        check_grad(got, r, slope, "bf16", "dlogits", tol)
+    far.copy_(x)
+    check_grad(bwd(far, t, lse, dlogp, out=far), r, slope, "bf16", "in place", tol)
+
+
+@gpu
 def test_a_wait_that_runs_out_is_reported(debug_env):
     """A negative limit makes every wait of a cluster for its peers give up at once.  The
     kernel has to end all the same, and the next call to be right."""

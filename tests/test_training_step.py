@@ -263,6 +263,42 @@ def test_a_step_of_all_of_them(kind):
 
 
 @gpu
+def test_a_captured_step_replays_on_new_inputs():
+    g = gen(7)
+    B, S = 2, 16
+    w = weights(g, torch.float32)
+    inv, sections = (10000.0 ** (-torch.arange(16, device="cuda") / 16)).float(), [6, 5, 5]
+
+    def inputs():
+        tokens = torch.randint(0, 503, (B, S), device="cuda", generator=g)
+        return [tokens, tokens.roll(-1, 1), torch.randint(0, 300, (3, B, S), device="cuda",
+                                                          generator=g),
+                -6 + 0.1 * randn(g, B, S), randn(g, B, S)]
+
+    def step(tokens, t, pos, old, adv):
+        loss, _ = ag.policy_loss(model(w, tokens, pos, inv, sections, True), t, old, adv, old,
+                                 kl_coef=0.05)
+        return (loss, *torch.autograd.grad(loss, list(w.values())))
+
+    held = inputs()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*held)
+    for _ in range(2):
+        new = inputs()
+        for a, b in zip(held, new):
+            a.copy_(b)
+        graph.replay()
+        for a, b in zip(out, step(*new)):
+            near(a.detach(), b.detach().double(), 5e-5)
+
+
+@gpu
 def test_one_pass_gradient_matches_the_autograd_step():
     # the C ABI's one-pass policy gradient is the autograd functions' gradient
     g = gen(6)
@@ -291,6 +327,23 @@ def test_arguments_are_checked_before_any_call():
                  lambda: ag.rms_norm_rope(q, None, torch.ones(8), None, pos, inv, [4])):
         with pytest.raises(ValueError):
             call()
+
+
+@gpu
+def test_positions_as_they_come():
+    # one row of positions for every axis, and positions held token by token
+    g = torch.Generator("cuda").manual_seed(3)
+    q = torch.randn(2, 9, 3, 32, device="cuda", generator=g)
+    inv = 100.0 ** (-torch.arange(16, device="cuda") / 16)
+    pos = torch.randint(0, 4000, (3, 2, 9), device="cuda", generator=g)
+    want, _ = ag.rope(q, None, pos, inv, [6, 5, 5])
+    apart = pos.permute(1, 2, 0).contiguous().permute(2, 0, 1)
+    assert torch.equal(ag.rope(q, None, apart, inv, [6, 5, 5])[0], want)
+    same = pos[:1].expand(3, -1, -1)
+    one, _ = ag.rope(q, None, pos[0], inv, [16])
+    assert torch.equal(ag.rope(q, None, same, inv, [6, 5, 5])[0], one)
+    flat, _ = ag.rope(q[0], None, same[:, 0], inv, [6, 5, 5])
+    assert torch.equal(flat, one[0])
 
 
 @gpu
