@@ -371,6 +371,40 @@ __device__ __forceinline__ void scale_packed(float (&o)[E], const uint4& x, cons
     put_pair(o, 2 * i, __fmul2_rn(products(xs[i], ws[i]), make_float2(rstd, rstd)));
 }
 
+// G lanes a row, 32 / G rows at a time: a power of two, or in the normed backward 5,
+// 6 or 10, of which a warp's last two lanes have no row.
+constexpr int kNoRow = 1 << 20;
+// Sum over a row's lanes, in a fixed order, for all of them.
+template <int G>
+__device__ __forceinline__ float row_sum(float v, int g) {
+  if constexpr ((G & (G - 1)) == 0) {
+    return group_sum<G>(v);
+  } else {
+    int n = G;
+#pragma unroll
+    for (int o = G < 8 ? 4 : 8; o > 0; o >>= 1) {
+      const float t = __shfl_down_sync(0xFFFFFFFFu, v, o);
+      if (g + o < n) v += t;
+      n = o;
+    }
+    return __shfl_sync(0xFFFFFFFFu, v, (int)(threadIdx.x & 31) - g);
+  }
+}
+// Sum of a lane's value over the rows, in a fixed order, for the first row's lanes.
+template <int G>
+__device__ __forceinline__ float rows_sum(float v) {
+  if constexpr ((G & (G - 1)) == 0) {
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  } else {
+    float s = v;
+#pragma unroll
+    for (int r = 1; r < 32 / G; ++r) s += __shfl_down_sync(0xFFFFFFFFu, v, r * G);
+    return s;
+  }
+}
+
 // Lane 4 k + a holds the position of token t0 + k on axis a (of up to eight
 // tokens), so that it can be asked for long before it is needed.
 __device__ __forceinline__ long long lane_position(const RopeParams& p, int64_t t0, int tokens) {
@@ -605,7 +639,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // in a uniform register
-  const int g = lane % G, rg = lane / G;
+  const int g = lane % G, rg = lane < RG * G ? lane / G : kNoRow;
   const int units = p.D / (2 * E);
   int va[L], vb[L];
 #pragma unroll
@@ -769,7 +803,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
         }
         load(stage);
         stage = stage + 1 == S ? 0 : stage + 1;
-        const float r = rsqrtf(group_sum<G>(ss.x + ss.y) * p.inv_d + p.eps);
+        const float r = rsqrtf(row_sum<G>(ss.x + ss.y, g) * p.inv_d + p.eps);
         // dgamma takes g x r; then g becomes g gamma
 #pragma unroll
         for (int k = 0; k < L; ++k) {
@@ -784,7 +818,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
           mul_all(db[k], db[k], wb[k]);
           dot_all(dot, db[k], b[k]);
         }
-        const float c = r * r * p.inv_d * group_sum<G>(dot.x + dot.y);
+        const float c = r * r * p.inv_d * row_sum<G>(dot.x + dot.y, g);
         if (!live) continue;
         TX* y = STEPPED ? yr : static_cast<TX*>(v.y) + (m.t0 + tok) * v.y_st + h * v.y_sh;
 #pragma unroll
@@ -806,11 +840,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_norm_bwd_kernel(RopePara
       for (int k = 0; k < L; ++k) {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-#pragma unroll
-          for (int o = G; o < 32; o <<= 1) {
-            ga[k][i] += __shfl_xor_sync(0xFFFFFFFFu, ga[k][i], o);
-            gb[k][i] += __shfl_xor_sync(0xFFFFFFFFu, gb[k][i], o);
-          }
+          ga[k][i] = rows_sum<G>(ga[k][i]);
+          gb[k][i] = rows_sum<G>(gb[k][i]);
           if (g + k * G < units && rg == 0) {
             red[warp * ld_red + va[k] * E + i] = ga[k][i];
             red[warp * ld_red + vb[k] * E + i] = gb[k][i];
@@ -978,6 +1009,7 @@ RopeKernel pick_shape(const RopeKey& k) {
     return k.block ? kernel_of<TX, TW, NORM, ADJ, BWD, E, G_, 1, true>() \
                    : kernel_of<TX, TW, NORM, ADJ, BWD, E, G_, 1, false>();
     RMSN_ROPE(4) RMSN_ROPE(8) RMSN_ROPE(16) RMSN_ROPE(32)
+    if constexpr (BWD) { RMSN_ROPE(5) RMSN_ROPE(6) RMSN_ROPE(10) }
 #undef RMSN_ROPE
     return nullptr;
   }

@@ -264,6 +264,11 @@ def test_many_tokens_and_heads():
     check_case(Case(5000, 6, 2, 64, 64, [12, 10, 10], order="interleaved"))
     check_case(Case(2, 300, 7, 128, 128, [24, 20, 20]))
     check_case(Case(700, 2, 1, 36, 36, [6, 6, 6]))
+    # several tokens an item, rows of 5, 6 and 10 lanes
+    check_case(Case(9000, 1, 1, 80, 80, [20, 10, 10]))
+    check_case(Case(8200, 2, 1, 96, 96, [16, 16, 16], norm=False))
+    check_case(Case(8200, 2, 1, 96, 96, [16, 16, 16], "adjacent"))
+    check_case(Case(8200, 1, 1, 80, 64, [16, 8, 8], "adjacent", xd="f32"))
 
 
 @gpu
