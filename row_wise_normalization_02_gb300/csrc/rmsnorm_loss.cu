@@ -526,7 +526,8 @@ __device__ __forceinline__ void copy_wait() {
 // points: 768 threads of it (896 where the ring is shorter) in CTAs as small as a
 // row's part allows, the ring of 64 bytes a thread and batch being what 227 KB hold.
 // (One CTA of 1024 threads per SM with the same ring 377 us; three quarters of a row
-// in the ring 362.)  An SM stores at most 32 bytes a clock, from wherever: 4.4 us for a row of 256 KB.
+// in the ring 362.)  An SM stores at most 32 bytes a clock, from wherever: 4.4 us for
+// a row of 256 KB.
 template <typename TX, int NT, int CL, int S>
 __global__ void __launch_bounds__(NT, 896 / NT) loss_stream_kernel(LossParams p) {
   constexpr int MODE = kLossPolicyGrad;
