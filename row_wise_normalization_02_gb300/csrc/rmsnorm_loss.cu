@@ -520,7 +520,7 @@ __device__ __forceinline__ void copy_wait() {
 // to fetch), so the data a step needs is always the S-th last group.
 //
 // What bounds it.  DRAM would take 285 us for 4096 x 131072 bf16 with a fifth of the
-// rows left out; this takes 343 (5.6 TB/s).  A CTA's passes are short, and its
+// rows left out; this takes 347 (5.6 TB/s).  A CTA's passes are short, and its
 // merges, the exchange with its peers and the loss between them -- some 8000 of a
 // row's 25000 clocks -- leave its warps idle, so an SM needs many CTAs at different
 // points: 768 threads of it (896 where the ring is shorter) in CTAs as small as a
